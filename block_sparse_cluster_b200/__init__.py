@@ -11,7 +11,7 @@ from __future__ import annotations
 import ctypes
 import os
 from dataclasses import dataclass
-from typing import Optional
+from typing import Optional, Tuple
 
 import torch
 
@@ -29,7 +29,8 @@ STATUS_NAMES = ["DA_OK", "DA_ERR_INVALID_ARG", "DA_ERR_SHAPE", "DA_ERR_DTYPE", "
 EXPORTS = ["da_version", "da_workspace_bytes", "da_schedule_bytes", "da_reassign", "da_mask_prepare",
            "da_attention", "da_device_status", "da_status_string", "da_reassign_noalloc", "da_compensation",
            "da_attention_prebuilt", "da_centroid_update", "da_cluster_spread", "da_attention_spread",
-           "da_attention_sip", "da_noalloc_device_status"]
+           "da_attention_sip", "da_noalloc_device_status", "da_rms_norm", "da_rms_norm_i8", "da_quantize_i8",
+           "da_linear_i8", "da_rope"]
 
 
 class DAError(RuntimeError):
@@ -54,7 +55,17 @@ class _Mask(ctypes.Structure):
                 ("schedule", ctypes.c_void_p)]
 
 
+class _HeadStrides(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int64), ("head", ctypes.c_int64), ("token", ctypes.c_int64)]
+
+
+class _RopePlan(ctypes.Structure):
+    _fields_ = [("axis_dims", ctypes.c_int * 3), ("grid", ctypes.c_int * 3), ("theta", ctypes.c_double),
+                ("pairing", ctypes.c_int)]
+
+
 _P = ctypes.c_void_p
+_I, _L, _F = ctypes.c_int, ctypes.c_int64, ctypes.c_float
 _lib.da_version.restype = ctypes.c_int
 _lib.da_workspace_bytes.restype = ctypes.c_size_t
 _lib.da_workspace_bytes.argtypes = [ctypes.POINTER(_Dims)]
@@ -87,6 +98,18 @@ _lib.da_reassign_noalloc.restype = ctypes.c_int
 _lib.da_reassign_noalloc.argtypes = [ctypes.POINTER(_Dims), _P, _P, _P, ctypes.POINTER(_Stats), _P]
 _lib.da_noalloc_device_status.restype = ctypes.c_int
 _lib.da_noalloc_device_status.argtypes = [_P]
+_lib.da_rms_norm.restype = _I
+_lib.da_rms_norm.argtypes = [_L, _I, _I, _P, _L, _P, _L, _P, _F, _P, _L, _P, _L, _P]
+_lib.da_rms_norm_i8.restype = _I
+_lib.da_rms_norm_i8.argtypes = [_L, _I, _I, _P, _L, _P, _L, _P, _F, _P, _L, _P, _L, _P, _P]
+_lib.da_quantize_i8.restype = _I
+_lib.da_quantize_i8.argtypes = [_I, _I, _I, _I, _I, _P, ctypes.POINTER(_HeadStrides), _P, _L, _P, _P]
+_lib.da_linear_i8.restype = _I
+_lib.da_linear_i8.argtypes = [_I, _I, _I, _I, _I, _P, _L, _P, _P, _L, _P, _P, _I, _P, ctypes.POINTER(_HeadStrides), _P,
+                              ctypes.c_size_t, _P]
+_lib.da_rope.restype = _I
+_lib.da_rope.argtypes = [ctypes.POINTER(_RopePlan), _I, _I, _I, _I, _I, _P, ctypes.POINTER(_HeadStrides), _P, _L, _P,
+                         _I, _F, _P, ctypes.POINTER(_HeadStrides), _P]
 _lib.da_device_status.restype = ctypes.c_int
 _lib.da_device_status.argtypes = [_P, _P]
 _lib.da_status_string.restype = ctypes.c_char_p
@@ -300,6 +323,189 @@ def da_device_status(ws: torch.Tensor, stream=None) -> int:
 def da_noalloc_device_status(stream=None) -> int:
     """Synchronise and return (and clear) the status word of da_reassign_noalloc's scratch."""
     return _lib.da_noalloc_device_status(_stream(stream))
+
+
+# Operators of the layer around the attention.  They take strided tensors, so the binding also reads
+# shapes, strides and devices; the calls run on the tensors' device, on its current stream by default.
+
+_CODES = {torch.bfloat16: DA_BF16, torch.float32: DA_F32}
+_INVALID_ARG, _SHAPE, _DTYPE = 1, 2, 3
+
+
+def _same_place(where: str, *tensors: Optional[torch.Tensor]) -> torch.device:
+    """The one CUDA device that holds all the tensors."""
+    device = tensors[0].device
+    for t in tensors:
+        if t is not None and (t.device != device or t.device.type != "cuda"):
+            raise DAError(_INVALID_ARG, f"{where}: tensors have to be on one CUDA device")
+    return device
+
+
+def _need(ok: bool, code: int, where: str, what: str):
+    if not ok:
+        raise DAError(code, f"{where}: {what}")
+
+
+def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
+    return None if t is None else t.data_ptr()
+
+
+def _rows(t: Optional[torch.Tensor], shape, dtype, where: str, what: str) -> int:
+    """The row stride of a [rows, width] tensor with contiguous rows (0 for None)."""
+    if t is None:
+        return 0
+    _need(tuple(t.shape) == tuple(shape), _SHAPE, where, f"{what} has to be {list(shape)}")
+    _need(t.dtype == dtype, _DTYPE, where, f"{what} has to be {dtype}")
+    _need(t.stride(1) == 1 or t.shape[1] == 1, _SHAPE, where, f"{what} needs contiguous rows")
+    return t.stride(0) if t.shape[0] > 1 else max(t.shape[1], t.stride(0))
+
+
+def _vector(t: Optional[torch.Tensor], n: int, dtype, where: str, what: str):
+    if t is not None:
+        _need(t.dim() == 1 and t.shape[0] == n, _SHAPE, where, f"{what} has to be [{n}]")
+        _need(t.dtype == dtype, _DTYPE, where, f"{what} has to be {dtype}")
+        _need(n == 1 or t.stride(0) == 1, _SHAPE, where, f"{what} has to be contiguous")
+
+
+def _head_strides(t: torch.Tensor, where: str, what: str) -> _HeadStrides:
+    """Strides of a [B, H, N, d] tensor with contiguous heads."""
+    _need(t.dim() == 4, _SHAPE, where, f"{what} has to be [B, H, N, d]")
+    _need(t.stride(3) == 1 or t.shape[3] == 1, _SHAPE, where, f"{what} needs a contiguous last dimension")
+    return _HeadStrides(t.stride(0), t.stride(1), t.stride(2))
+
+
+def _on(device: torch.device, stream, f, *args) -> int:
+    """Calls f(*args, stream) with `device` current."""
+    if device.index == torch.cuda.current_device():
+        return f(*args, _stream(stream))
+    with torch.cuda.device(device):
+        return f(*args, _stream(stream))
+
+
+def _norm_args(where, x, weight, residual, sum_out, eps):
+    _need(x.dim() == 2, _SHAPE, where, "x has to be [rows, width]")
+    _need(x.dtype in _CODES, _DTYPE, where, "x has to be bfloat16 or float32")
+    rows, width = x.shape
+    _vector(weight, width, x.dtype, where, "weight")
+    return (rows, width, _CODES[x.dtype], x.data_ptr(), _rows(x, x.shape, x.dtype, where, "x"), _ptr(residual),
+            _rows(residual, x.shape, x.dtype, where, "residual"), _ptr(weight), float(eps), _ptr(sum_out),
+            _rows(sum_out, x.shape, x.dtype, where, "sum_out"))
+
+
+def da_rms_norm(x: torch.Tensor, weight: Optional[torch.Tensor], out: torch.Tensor,
+                residual: Optional[torch.Tensor] = None, sum_out: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                stream=None) -> torch.Tensor:
+    """out = v / sqrt(mean(v^2) + eps) * weight with v = x + residual, rows [rows, width] of bf16 or
+    fp32; sum_out takes v (the residual stream; it may be the residual's or x's own buffer)."""
+    where = "da_rms_norm"
+    device = _same_place(where, x, weight, out, residual, sum_out)
+    _check(_on(device, stream, _lib.da_rms_norm, *_norm_args(where, x, weight, residual, sum_out, eps), out.data_ptr(),
+               _rows(out, x.shape, x.dtype, where, "out")), where)
+    return out
+
+
+def da_rms_norm_i8(x: torch.Tensor, weight: Optional[torch.Tensor], q: torch.Tensor, scale: torch.Tensor,
+                   residual: Optional[torch.Tensor] = None, sum_out: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                   stream=None):
+    """da_rms_norm with its output in 8-bit codes: q [rows, width] int8 (rows may be padded: a row
+    stride that is a multiple of 16 suits da_linear_i8), scale [rows] fp32, output = q * scale."""
+    where = "da_rms_norm_i8"
+    device = _same_place(where, x, weight, q, scale, residual, sum_out)
+    args = _norm_args(where, x, weight, residual, sum_out, eps)
+    _vector(scale, x.shape[0], torch.float32, where, "scale")
+    _check(_on(device, stream, _lib.da_rms_norm_i8, *args, q.data_ptr(), _rows(q, x.shape, torch.int8, where, "q"),
+               scale.data_ptr()), where)
+    return q, scale
+
+
+def da_quantize_i8(x: torch.Tensor, q: torch.Tensor, scale: torch.Tensor, stream=None):
+    """Rows in 8-bit codes with a scale each, x ~ q * scale: x is [rows, width], or the attention's
+    [B, H, N, d], whose token (b, n) becomes row b * N + n of q [B*N, H*d] (heads side by side)."""
+    where = "da_quantize_i8"
+    device = _same_place(where, x, q, scale)
+    _need(x.dtype in _CODES, _DTYPE, where, "x has to be bfloat16 or float32")
+    if x.dim() == 2:
+        strides = _HeadStrides(0, 0, _rows(x, x.shape, x.dtype, where, "x"))
+        B, H, N, d = 1, 1, x.shape[0], x.shape[1]
+    else:
+        strides = _head_strides(x, where, "x")
+        B, H, N, d = x.shape
+    _vector(scale, B * N, torch.float32, where, "scale")
+    _check(_on(device, stream, _lib.da_quantize_i8, B, H, N, d, _CODES[x.dtype], x.data_ptr(), ctypes.byref(strides),
+               q.data_ptr(), _rows(q, (B * N, H * d), torch.int8, where, "q"), scale.data_ptr()), where)
+    return q, scale
+
+
+def da_linear_i8(x: torch.Tensor, x_scale: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor, out: torch.Tensor,
+                 ws: torch.Tensor, bias: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """out = (x w^T) * x_scale * w_scale + bias for int8 codes x [M, K] and w [C, K], fp32 scales [M]
+    and [C], fp32 bias [C]; out is [M, C] or, as heads, [B, H, N, d] with B*N = M, H*d = C, of bf16 or
+    fp32.  ws: a zero-filled workspace of at least 256 bytes (one of `workspace(dims)` serves too)."""
+    where = "da_linear_i8"
+    device = _same_place(where, x, x_scale, w, w_scale, out, ws, bias)
+    _need(out.dtype in _CODES, _DTYPE, where, "out has to be bfloat16 or float32")
+    _need(x.dim() == 2 and w.dim() == 2, _SHAPE, where, "x and w have to be matrices")
+    (M, K), C = x.shape, w.shape[0]
+    if out.dim() == 2:
+        strides = _HeadStrides(0, 0, _rows(out, (M, C), out.dtype, where, "out"))
+        B, H, N, d = 1, 1, M, C
+    else:
+        strides = _head_strides(out, where, "out")
+        B, H, N, d = out.shape
+        _need(B * N == M and H * d == C, _SHAPE, where, f"out has to hold {M} tokens of {C} channels")
+    _vector(x_scale, M, torch.float32, where, "x_scale")
+    _vector(w_scale, C, torch.float32, where, "w_scale")
+    _vector(bias, C, torch.float32, where, "bias")
+    _check(_on(device, stream, _lib.da_linear_i8, B, N, H, d, K, x.data_ptr(), _rows(x, (M, K), torch.int8, where, "x"),
+               x_scale.data_ptr(), w.data_ptr(), _rows(w, (C, K), torch.int8, where, "w"), w_scale.data_ptr(),
+               _ptr(bias), _CODES[out.dtype], out.data_ptr(), ctypes.byref(strides), ws.data_ptr(),
+               ws.numel() * ws.element_size()), where)
+    return out
+
+
+PAIRINGS = {"adjacent": 0, "halves": 1}
+
+
+@dataclass(frozen=True)
+class Rope:
+    """Rotary positions: the elements of a head that time, height and width turn, the token grid
+    (unused where positions are given), the base of the frequencies and how pairs lie in a head."""
+    axes: Tuple[int, int, int]
+    grid: Tuple[int, int, int] = (0, 0, 0)
+    theta: float = 10000.0
+    pairing: str = "adjacent"
+
+    def c(self) -> _RopePlan:
+        if len(self.axes) != 3 or len(self.grid) != 3 or self.pairing not in PAIRINGS:
+            raise DAError(_INVALID_ARG, "Rope: three axes, a grid of three and a pairing of " + " or ".join(PAIRINGS))
+        return _RopePlan((_I * 3)(*self.axes), (_I * 3)(*self.grid), self.theta, PAIRINGS[self.pairing])
+
+
+def da_rope(x: torch.Tensor, out: torch.Tensor, rope: Rope, positions: Optional[torch.Tensor] = None,
+            weight: Optional[torch.Tensor] = None, eps: float = 1e-6, stream=None) -> torch.Tensor:
+    """Rotary positions of x [B, H, N, d] (any strides with contiguous heads, such as a view of a
+    projection's token rows) into out, which may be x.  positions: int32 [N, 3] or [B, N, 3]; None:
+    the rope's grid.  weight [d] or [H*d]: the head or the token is normed first."""
+    where = "da_rope"
+    device = _same_place(where, x, out, positions, weight)
+    _need(x.dtype in _CODES, _DTYPE, where, "x has to be bfloat16 or float32")
+    _need(out.dtype == x.dtype and (weight is None or weight.dtype == x.dtype), _DTYPE, where,
+          "out and weight have to be of x's type")
+    xs, os_ = _head_strides(x, where, "x"), _head_strides(out, where, "out")
+    _need(out.shape == x.shape, _SHAPE, where, "out has to be of x's shape")
+    B, H, N, d = x.shape
+    batch = 0
+    if positions is not None:
+        _need(positions.dtype == torch.int32, _DTYPE, where, "positions have to be int32")
+        _need(tuple(positions.shape) in ((N, 3), (B, N, 3)) and positions.is_contiguous(), _SHAPE, where,
+              "positions have to be contiguous [N, 3] or [B, N, 3]")
+        batch = 3 * N if positions.dim() == 3 else 0
+    if weight is not None:
+        _vector(weight, weight.numel(), x.dtype, where, "weight")
+    _check(_on(device, stream, _lib.da_rope, ctypes.byref(rope.c()), B, H, N, d, _CODES[x.dtype], x.data_ptr(),
+               ctypes.byref(xs), _ptr(positions), batch, _ptr(weight), 0 if weight is None else weight.numel(), float(eps),
+               out.data_ptr(), ctypes.byref(os_)), where)
+    return out
 
 
 class DecoupledAttention:

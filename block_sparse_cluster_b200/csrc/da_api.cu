@@ -5,6 +5,7 @@
 #include <stdint.h>
 
 #include "da.h"
+#include "da_common.cuh"
 #include "da_internal.h"
 
 using namespace da;
@@ -86,6 +87,101 @@ da_status check_mask(const Dims& g, const da_block_mask* mask) {
 }
 
 da_status cuda_status(cudaError_t e) { return e == cudaSuccess ? DA_OK : DA_ERR_CUDA; }
+
+// A strided tensor of the layer operators: up to three outer dimensions over `inner` contiguous
+// elements of `size` bytes.
+struct View {
+  const void* p;
+  long long inner;
+  int size;
+  long long n[3], stride[3];
+
+  bool fits() const {   // strides and extents whose byte offsets stay far inside 64 bits
+    for (int i = 0; i < 3; ++i)
+      if (stride[i] < 0 || stride[i] > (1LL << 40) || n[i] >= (1LL << 31)) return false;
+    return span() < (1LL << 46);
+  }
+  long long span() const {   // elements from the first to the last, both included
+    long long s = inner;
+    for (int i = 0; i < 3; ++i)
+      if (n[i] > 1) s += (n[i] - 1) * stride[i] < 0 ? (1LL << 46) : (n[i] - 1) * stride[i];
+    return s;
+  }
+  // No element twice: each outer dimension, from the smallest stride up, steps over what lies below it.
+  bool distinct() const {
+    int order[3] = {0, 1, 2};
+    for (int i = 0; i < 3; ++i)
+      for (int j = i + 1; j < 3; ++j)
+        if (stride[order[j]] < stride[order[i]]) { const int t = order[i]; order[i] = order[j]; order[j] = t; }
+    long long s = inner;
+    for (int i = 0; i < 3; ++i) {
+      const int k = order[i];
+      if (n[k] <= 1) continue;
+      if (stride[k] < s) return false;
+      s += (n[k] - 1) * stride[k];
+    }
+    return true;
+  }
+  bool element_aligned() const { return reinterpret_cast<uintptr_t>(p) % size == 0; }
+  bool aligned16() const {   // every run of `inner` elements starts on 16 bytes
+    bool ok = reinterpret_cast<uintptr_t>(p) % 16 == 0 && inner * size % 16 == 0;
+    for (int i = 0; i < 3; ++i) ok = ok && (n[i] <= 1 || stride[i] * size % 16 == 0);
+    return ok;
+  }
+};
+
+View matrix(const void* p, int size, long long rows, long long width, long long stride) {
+  return View{p, width, size, {1, 1, rows}, {0, 0, stride}};
+}
+
+View heads(const void* p, int size, int B, int H, int N, int d, const da_head_strides& s) {
+  return View{p, d, size, {B, H, N}, {s.batch, s.head, s.token}};
+}
+
+// An output and another tensor: apart in memory, or (in_place) the very same elements.
+bool apart(const View& o, const View& v, bool in_place) {
+  if (!v.p) return true;
+  const uintptr_t o0 = reinterpret_cast<uintptr_t>(o.p), v0 = reinterpret_cast<uintptr_t>(v.p);
+  const uintptr_t o1 = o0 + (uintptr_t)(o.span() * o.size), v1 = v0 + (uintptr_t)(v.span() * v.size);
+  if (o1 <= v0 || v1 <= o0) return true;
+  if (!in_place || o0 != v0 || o.inner != v.inner || o.size != v.size) return false;
+  for (int i = 0; i < 3; ++i)
+    if (o.n[i] > 1 && o.stride[i] != v.stride[i]) return false;
+  return true;
+}
+
+constexpr int kMaxRowWidth = 16384;   // a row is held in one block's registers
+
+da_status check_dtype(da_dtype t) { return t == DA_BF16 || t == DA_F32 ? DA_OK : DA_ERR_DTYPE; }
+int element_size(da_dtype t) { return t == DA_BF16 ? 2 : 4; }
+
+// Shared by da_rms_norm and da_rms_norm_i8 (scale non-null): out and its rows are elements or codes.
+da_status rms_norm(int64_t rows, int width, da_dtype dtype, const void* x, int64_t x_stride, const void* residual,
+                   int64_t residual_stride, const void* weight, float eps, void* sum_out, int64_t sum_stride,
+                   void* out, int64_t out_stride, float* scale, bool codes, da_stream stream) {
+  if (rows <= 0 || width <= 0 || !x || !out || (codes && !scale) || (sum_out && !residual)) return DA_ERR_INVALID_ARG;
+  if (!(eps >= 0.f) || eps > 3e38f) return DA_ERR_INVALID_ARG;
+  da_status st = check_dtype(dtype);
+  if (st != DA_OK) return st;
+  if (width > kMaxRowWidth) return DA_ERR_UNSUPPORTED;
+  const int size = element_size(dtype);
+  const View vx = matrix(x, size, rows, width, x_stride), vr = matrix(residual, size, rows, width, residual_stride);
+  const View vw = matrix(weight, size, 1, width, 0), vs = matrix(sum_out, size, rows, width, sum_stride);
+  const View vo = matrix(out, codes ? 1 : size, rows, width, out_stride), vc = matrix(scale, 4, rows, 1, 1);
+  if (!vx.fits() || !vo.fits() || (residual && !vr.fits()) || (sum_out && !vs.fits())) return DA_ERR_SHAPE;
+  if (!vo.distinct() || (sum_out && !vs.distinct())) return DA_ERR_SHAPE;
+  if (!vx.element_aligned() || !vr.element_aligned() || !vw.element_aligned() || !vs.element_aligned() ||
+      !vo.element_aligned() || !vc.element_aligned())
+    return DA_ERR_ALIGNMENT;
+  const bool ok = apart(vo, vx, !codes) && apart(vo, vr, !codes) && apart(vo, vw, false) && apart(vo, vs, false) &&
+                  apart(vo, vc, false) &&
+                  (!sum_out || (apart(vs, vx, true) && apart(vs, vr, true) && apart(vs, vw, false) && apart(vs, vc, false))) &&
+                  (!codes || (apart(vc, vx, false) && apart(vc, vr, false) && apart(vc, vw, false)));
+  if (!ok) return DA_ERR_INVALID_ARG;
+  return cuda_status(launch_rms_norm(dtype == DA_BF16, rows, width, x, x_stride, residual, residual_stride, weight, eps,
+                                     sum_out, sum_stride, out, out_stride, codes ? scale : nullptr,
+                                     reinterpret_cast<cudaStream_t>(stream)));
+}
 
 }  // namespace
 
@@ -334,6 +430,105 @@ da_status da_attention_sip(const da_dims* dims, const void* Q, const void* K, co
     e = launch_attention_tc(g, Q, K, V, mask->kv_idx, mask->kv_cnt, mask->max_sel, sched, K, StatsPtrs{}, scale, O,
                             lse, status, static_cast<char*>(ws) + L.comp, incl, nullptr, s);
   return cuda_status(e);
+}
+
+da_status da_rms_norm(int64_t rows, int width, da_dtype dtype, const void* x, int64_t x_stride, const void* residual,
+                      int64_t residual_stride, const void* weight, float eps, void* sum_out, int64_t sum_stride,
+                      void* out, int64_t out_stride, da_stream stream) {
+  NvtxRange nvtx("da_rms_norm");
+  return rms_norm(rows, width, dtype, x, x_stride, residual, residual_stride, weight, eps, sum_out, sum_stride, out,
+                  out_stride, nullptr, false, stream);
+}
+
+da_status da_rms_norm_i8(int64_t rows, int width, da_dtype dtype, const void* x, int64_t x_stride,
+                         const void* residual, int64_t residual_stride, const void* weight, float eps, void* sum_out,
+                         int64_t sum_stride, int8_t* q, int64_t q_stride, float* scale, da_stream stream) {
+  NvtxRange nvtx("da_rms_norm_i8");
+  return rms_norm(rows, width, dtype, x, x_stride, residual, residual_stride, weight, eps, sum_out, sum_stride, q,
+                  q_stride, scale, true, stream);
+}
+
+da_status da_quantize_i8(int B, int H, int N, int d, da_dtype dtype, const void* x, const da_head_strides* x_strides,
+                         int8_t* q, int64_t q_stride, float* scale, da_stream stream) {
+  NvtxRange nvtx("da_quantize_i8");
+  if (B <= 0 || H <= 0 || N <= 0 || d <= 0 || !x || !x_strides || !q || !scale) return DA_ERR_INVALID_ARG;
+  const da_status st = check_dtype(dtype);
+  if (st != DA_OK) return st;
+  if ((long long)H * d > kMaxRowWidth) return DA_ERR_UNSUPPORTED;
+  const long long rows = (long long)B * N;
+  const View vx = heads(x, element_size(dtype), B, H, N, d, *x_strides);
+  const View vq = matrix(q, 1, rows, H * d, q_stride), vc = matrix(scale, 4, rows, 1, 1);
+  if (rows >= (1LL << 31) || !vx.fits() || !vq.fits() || !vq.distinct()) return DA_ERR_SHAPE;
+  if (!vx.element_aligned() || !vc.element_aligned()) return DA_ERR_ALIGNMENT;
+  if (!apart(vq, vx, false) || !apart(vq, vc, false) || !apart(vc, vx, false)) return DA_ERR_INVALID_ARG;
+  return cuda_status(launch_quantize_i8(dtype == DA_BF16, B, H, N, d, x, *x_strides, q, q_stride, scale,
+                                        reinterpret_cast<cudaStream_t>(stream)));
+}
+
+da_status da_linear_i8(int B, int N, int H, int d, int K, const int8_t* x, int64_t x_stride, const float* x_scale,
+                       const int8_t* w, int64_t w_stride, const float* w_scale, const float* bias, da_dtype out_dtype,
+                       void* out, const da_head_strides* out_strides, void* ws, size_t ws_bytes, da_stream stream) {
+  NvtxRange nvtx("da_linear_i8");
+  if (B <= 0 || N <= 0 || H <= 0 || d <= 0 || K <= 0 || !x || !x_scale || !w || !w_scale || !out || !out_strides || !ws)
+    return DA_ERR_INVALID_ARG;
+  const da_status st = check_dtype(out_dtype);
+  if (st != DA_OK) return st;
+  // 128 * 128 * K has to stay below 2^31
+  if (K > 131071) return DA_ERR_UNSUPPORTED;
+  const long long M = (long long)B * N, channels = (long long)H * d;
+  if (M >= (1LL << 31) || channels > (1 << 22) - 64) return DA_ERR_SHAPE;
+  const View vx = matrix(x, 1, M, K, x_stride), vw = matrix(w, 1, channels, K, w_stride);
+  const View vsx = matrix(x_scale, 4, M, 1, 1), vsw = matrix(w_scale, 4, channels, 1, 1);
+  const View vb = matrix(bias, 4, channels, 1, 1);
+  const View vo = heads(out, element_size(out_dtype), B, H, N, d, *out_strides);
+  if (!vx.fits() || !vw.fits() || !vo.fits() || !vo.distinct()) return DA_ERR_SHAPE;
+  if (!vsx.element_aligned() || !vsw.element_aligned() || !vb.element_aligned() || !vo.element_aligned() || !aligned16(ws))
+    return DA_ERR_ALIGNMENT;
+  if (ws_bytes < kStatusWords * sizeof(int)) return DA_ERR_WORKSPACE;
+  if (!apart(vo, vx, false) || !apart(vo, vw, false) || !apart(vo, vsx, false) || !apart(vo, vsw, false) ||
+      !apart(vo, vb, false) || !apart(vo, matrix(ws, 1, 1, kStatusWords * sizeof(int), 0), false))
+    return DA_ERR_INVALID_ARG;
+  const LinearArgs a{x, w, x_scale, w_scale, bias, out, M, (int)channels, K, d, N,
+                     x_stride, w_stride, out_strides->batch, out_strides->head, out_strides->token};
+  return cuda_status(launch_linear_i8_simt(out_dtype == DA_BF16, a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+da_status da_rope(const da_rope_plan* plan, int B, int H, int N, int d, da_dtype dtype, const void* x,
+                  const da_head_strides* x_strides, const int32_t* positions, int64_t positions_batch,
+                  const void* weight, int weight_width, float eps, void* out, const da_head_strides* out_strides,
+                  da_stream stream) {
+  NvtxRange nvtx("da_rope");
+  if (!plan || B <= 0 || H <= 0 || N <= 0 || d <= 0 || !x || !x_strides || !out || !out_strides)
+    return DA_ERR_INVALID_ARG;
+  da_status st = check_dtype(dtype);
+  if (st != DA_OK) return st;
+  if (d != 64 && d != 128) return DA_ERR_UNSUPPORTED;
+  if (plan->pairing != DA_ROPE_ADJACENT && plan->pairing != DA_ROPE_HALVES) return DA_ERR_INVALID_ARG;
+  if (!(plan->theta > 0.0) || !(plan->theta < 1e30)) return DA_ERR_INVALID_ARG;
+  long long dims = 0, cells = 1;
+  for (int u = 0; u < 3; ++u) {
+    if (plan->axis_dims[u] < 0 || plan->axis_dims[u] % 2 != 0) return DA_ERR_SHAPE;
+    dims += plan->axis_dims[u];
+    if (!positions) {
+      if (plan->grid[u] <= 0) return DA_ERR_SHAPE;
+      if ((cells *= plan->grid[u]) >= (1LL << 31)) return DA_ERR_SHAPE;
+    }
+  }
+  if (dims != d) return DA_ERR_SHAPE;
+  if (weight && ((weight_width != d && weight_width != (long long)H * d) || !(eps >= 0.f) || eps > 3e38f))
+    return weight_width != d && weight_width != (long long)H * d ? DA_ERR_SHAPE : DA_ERR_INVALID_ARG;
+  if (weight && weight_width != d && weight_width > kMaxRowWidth) return DA_ERR_UNSUPPORTED;
+  const int size = element_size(dtype);
+  const View vx = heads(x, size, B, H, N, d, *x_strides), vo = heads(out, size, B, H, N, d, *out_strides);
+  const View vw = matrix(weight, size, 1, weight ? weight_width : 1, 0);
+  const View vp = View{positions, 3, 4, {1, B, N}, {0, positions_batch, 3}};
+  if ((long long)B * N >= (1LL << 31) || !vx.fits() || !vo.fits() || !vo.distinct()) return DA_ERR_SHAPE;
+  if (positions && (!vp.fits() || (positions_batch != 0 && positions_batch < 3LL * N))) return DA_ERR_SHAPE;
+  if (!vx.aligned16() || !vo.aligned16() || reinterpret_cast<uintptr_t>(weight) % 16 != 0 || !vp.element_aligned())
+    return DA_ERR_ALIGNMENT;
+  if (!apart(vo, vx, true) || !apart(vo, vw, false) || !apart(vo, vp, false)) return DA_ERR_INVALID_ARG;
+  return cuda_status(launch_rope(dtype == DA_BF16, *plan, B, H, N, d, x, *x_strides, positions, positions_batch, weight,
+                                 weight_width, eps, out, *out_strides, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 da_status da_device_status(void* ws, da_stream stream) {

@@ -67,6 +67,32 @@ cudaError_t launch_attention_tc(const Dims& g, const void* Q, const void* K, con
 cudaError_t launch_comp_build(const Dims& g, const int32_t* kv_idx, const int32_t* kv_cnt, int max_sel,
                               const StatsPtrs& st, void* out, cudaStream_t s);
 
+// rows.cu: a scale pointer selects the form with 8-bit codes
+cudaError_t launch_rms_norm(bool bf16, long long rows, int width, const void* x, long long x_stride,
+                            const void* residual, long long r_stride, const void* weight, float eps, void* sum_out,
+                            long long sum_stride, void* out, long long out_stride, float* scale, cudaStream_t s);
+cudaError_t launch_quantize_i8(bool bf16, int B, int H, int N, int d, const void* x, const da_head_strides& xs,
+                               int8_t* q, long long q_stride, float* scale, cudaStream_t s);
+
+// rope.cu
+cudaError_t launch_rope(bool bf16, const da_rope_plan& plan, int B, int H, int N, int d, const void* x,
+                        const da_head_strides& xs, const int32_t* positions, long long pos_batch, const void* weight,
+                        int weight_width, float eps, void* out, const da_head_strides& os, cudaStream_t s);
+
+// linear_i8_simt.cu: out[m, n] at (m / tokens) * out_batch + (n / d) * out_head + (m % tokens) * out_token + n % d
+struct LinearArgs {
+  const int8_t* x;
+  const int8_t* w;
+  const float* x_scale;
+  const float* w_scale;
+  const float* bias;      // or null
+  void* out;
+  long long M;
+  int N, K, d, tokens;
+  long long x_stride, w_stride, out_batch, out_head, out_token;
+};
+cudaError_t launch_linear_i8_simt(bool bf16, const LinearArgs& a, cudaStream_t s);
+
 // simt_f32.cu / simt_bf16.cu
 #define DA_SIMT_DECL(SUFFIX)                                                                                 \
   cudaError_t launch_assign_simt_##SUFFIX(const Dims& g, const void* K, const void* cent, int32_t* assign,    \

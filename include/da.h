@@ -291,6 +291,122 @@ DA_API da_status da_reassign_noalloc(const da_dims* dims, const void* K, const v
  * synchronisation or the read failed).  Allocates nothing. */
 DA_API da_status da_noalloc_device_status(da_stream stream);
 
+/*
+ * Operators of the layer around the attention: from hidden states to Q, K and V and from O back.
+ *
+ *   da_rms_norm(_i8) -> da_linear_i8 (Q and K as token rows, V as heads) -> da_rope (norm of Q and
+ *   K, rotary positions, heads) -> da_reassign + da_attention -> da_quantize_i8 -> da_linear_i8
+ *
+ * Conventions beside the shared ones above: every tensor has strides, in elements, and its
+ * innermost dimension is contiguous.  Sizes are positive (DA_ERR_INVALID_ARG otherwise); a row or
+ * token index stays below 2^31 and every stride below 2^40 (DA_ERR_SHAPE otherwise).  Inputs may
+ * repeat rows (stride 0); an output whose strides make two of its elements share memory is
+ * DA_ERR_SHAPE.  An output may share memory with an input only where a call says so, and then
+ * both are the same elements (base and strides); any other overlap of the address ranges is
+ * DA_ERR_INVALID_ARG.  Base pointers are aligned to their element, unless a call asks for
+ * 16 bytes (DA_ERR_ALIGNMENT).  No call allocates, synchronises or keeps anything; all can be
+ * captured into a CUDA graph.  Results do not depend on the launch: the same inputs give the same
+ * bits.  These are inference operators, like the attention: none has a backward pass.
+ */
+
+/* Strides, in elements, of a tensor whose element (b, h, n, t) lies at b * batch + h * head + n * token + t. */
+typedef struct {
+  int64_t batch, head, token;
+} da_head_strides;
+
+/*
+ * Root-mean-square norm of rows, with the residual's addition:
+ *   v = x + residual,   out = v / sqrt(mean(v^2) + eps) * weight,   sum_out = v.
+ * x, residual (NULL: none), out, sum_out (NULL: not written; needs residual): [rows, width] of
+ * dtype, rows their stride apart; weight: [width] of dtype (NULL: ones).  v, the sum of squares and
+ * the products are held in fp32 (v is not rounded to dtype before the norm); out and sum_out are rounded
+ * once.  out may be x or residual, sum_out may be x or residual (the residual stream updated in
+ * place), but not the same buffer.  width <= 16384 (DA_ERR_UNSUPPORTED above); eps >= 0.  A row with an infinity
+ * or NaN gives what the formula gives; so does one whose squares leave fp32's range (|v| above about 1e19).
+ */
+DA_API da_status da_rms_norm(int64_t rows, int width, da_dtype dtype, const void* x, int64_t x_stride,
+                             const void* residual, int64_t residual_stride, const void* weight, float eps,
+                             void* sum_out, int64_t sum_stride, void* out, int64_t out_stride, da_stream stream);
+
+/*
+ * da_rms_norm with its output in 8-bit codes and one fp32 scale per row: with t = v * weight and
+ * m = max |t| over the row,
+ *   q = nearest integer to 127 t / m (ties to even),   scale = m / (127 sqrt(mean(v^2) + eps)),
+ * so that q * scale is the norm's output to half a step.  q is taken from the exact quotient (fp64
+ * where fp32 cannot tell the two sides of a border apart).  A row of zeros gives q = 0, scale = 0; a row with an
+ * infinity or NaN (or whose t leaves fp32's range) gives q = 0, scale = NaN, so that products of it
+ * are NaN.  q: [rows, width] int8, q_stride elements apart (a multiple of 16 for da_linear_i8's tensor-core path); bytes
+ * between width and q_stride are left as they were.  scale: [rows] fp32.  Other arguments and errors as in da_rms_norm,
+ * but q and scale share memory with nothing.
+ */
+DA_API da_status da_rms_norm_i8(int64_t rows, int width, da_dtype dtype, const void* x, int64_t x_stride,
+                                const void* residual, int64_t residual_stride, const void* weight, float eps,
+                                void* sum_out, int64_t sum_stride, int8_t* q, int64_t q_stride, float* scale,
+                                da_stream stream);
+
+/*
+ * Rows in 8-bit codes without a norm: the H * d elements of token (b, n) become row b * N + n of q,
+ * with m = max |x| over the row, q = nearest integer to 127 x / m (ties to even), scale = m / 127.
+ * x: [B,H,N,d] of dtype with the given strides (the attention's O; a matrix of weights is B = H = 1,
+ * one row per output channel).  q: [B*N, H*d] int8, scale: [B*N] fp32; rows of zeros and rows
+ * with infinities or NaN as in da_rms_norm_i8.  H * d <= 16384.
+ */
+DA_API da_status da_quantize_i8(int B, int H, int N, int d, da_dtype dtype, const void* x,
+                                const da_head_strides* x_strides, int8_t* q, int64_t q_stride, float* scale,
+                                da_stream stream);
+
+/*
+ * Product of 8-bit integer matrices with scales for each token and channel: for token (b, n), row
+ * m = b * N + n of x, and channel c = h * d + t, row c of w,
+ *   out[b,h,n,t] = (sum_k x[m,k] w[c,k]) * x_scale[m] * w_scale[c] + bias[c].
+ * The sum is exact (32-bit integers, K <= 131071, else DA_ERR_UNSUPPORTED); scales and bias apply in fp32 and the
+ * result is rounded once to out_dtype.  x: [B*N, K] int8, w: [H*d, K] int8, rows their strides
+ * apart; x_scale: [B*N], w_scale: [H*d], bias: [H*d] (NULL: none), fp32; out: [B,H,N,d] with the
+ * given strides, so that V is written as the attention reads it; a plain matrix [M, C] is B = 1,
+ * N = M, H = 1, d = C.  H * d < 2^22.  Codes are taken as they are, -128 included.
+ * Where x and w and their strides are multiples of 16 bytes the product runs on the tensor cores,
+ * otherwise on the CUDA cores.  ws: device workspace of at least 256 bytes, 16-byte aligned,
+ * zero-filled once (one of da_workspace_bytes serves too): its status word takes a bounded wait
+ * that gave up (DA_ERR_TIMEOUT from da_device_status).
+ */
+DA_API da_status da_linear_i8(int B, int N, int H, int d, int K, const int8_t* x, int64_t x_stride,
+                              const float* x_scale, const int8_t* w, int64_t w_stride, const float* w_scale,
+                              const float* bias, da_dtype out_dtype, void* out, const da_head_strides* out_strides,
+                              void* ws, size_t ws_bytes, da_stream stream);
+
+typedef enum {
+  DA_ROPE_ADJACENT = 0,   /* pair p is elements 2p, 2p + 1 of the head */
+  DA_ROPE_HALVES = 1      /* pair p is elements p, p + d/2 */
+} da_rope_pairing;
+
+/* Rotary positions over time, height and width (host memory, read during the call). */
+typedef struct {
+  int axis_dims[3];   /* elements of a head that each axis turns: even, sum d; an axis may have none */
+  int grid[3];        /* token n of the grid has position (n / (grid[1] grid[2]), n / grid[2] % grid[1], n % grid[2]);
+                         used, and positive, where no positions are given */
+  double theta;       /* frequency j of an axis of D elements is theta^(-2j / D); 0 < theta < 1e30 */
+  int pairing;        /* a da_rope_pairing */
+} da_rope_plan;
+
+/*
+ * Rotary positions over several axes, after an optional norm: every pair (a, b) of a head, with
+ * the pairs given to the axes in order (the first axis_dims[0] / 2 to time, ...), becomes
+ * (a cos f - b sin f, a sin f + b cos f), f = position on its axis times the pair's frequency.
+ * x, out: [B,H,N,d] of dtype with their strides (x may be a slice of a projection's token rows,
+ * out the attention's [B,H,N,d]); bases, strides and weight on 16 bytes.  d is 64 or 128.
+ * positions: [N,3] int32 (time, height, width; any int32, negative ones turn back), one list for each
+ * batch entry positions_batch elements apart (0: one list for all), or NULL: the plan's grid.  Tokens behind
+ * the grid (text behind a video) are not turned: they are copied, or normed only.
+ * weight: NULL, or the norm's weight of dtype, with x first replaced by x / sqrt(mean(x^2) + eps) *
+ * weight: the mean over the head's d elements if weight_width = d, over all of a token's heads if
+ * weight_width = H * d (<= 16384).  Angles are formed in fp64; norm and rotation in fp32, rounded once.
+ * out may be x.
+ */
+DA_API da_status da_rope(const da_rope_plan* plan, int B, int H, int N, int d, da_dtype dtype, const void* x,
+                         const da_head_strides* x_strides, const int32_t* positions, int64_t positions_batch,
+                         const void* weight, int weight_width, float eps, void* out,
+                         const da_head_strides* out_strides, da_stream stream);
+
 /* Synchronise `stream`, then report and clear the workspace status word:
  * DA_OK, DA_ERR_TIMEOUT, DA_ERR_DEVICE_INDEX or DA_ERR_RANGE (or DA_ERR_CUDA if the
  * synchronisation itself failed). */

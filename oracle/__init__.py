@@ -67,7 +67,7 @@ import numpy as np
 __all__ = [
     "reassign", "block_ranges", "block_histogram", "block_entries", "cluster_totals",
     "complement_stats", "attention_qblock", "attention", "lloyd_step", "kmeans", "sse",
-    "cluster_spread", "attention_sip_qblock",
+    "cluster_spread", "attention_sip_qblock", "rms_norm", "row_codes", "rms_norm_i8", "linear_i8", "rope_angles", "rope",
 ]
 
 
@@ -337,3 +337,62 @@ def kmeans(K, init, iters: int) -> Tuple[np.ndarray, np.ndarray]:
     for _ in range(iters):
         c, a = lloyd_step(K, c)
     return c, a
+
+
+# ---------------------------------------------------------------------------
+# operators of the layer around the attention
+
+def rms_norm(x, residual=None, weight=None, eps: float = 1e-6) -> Tuple[np.ndarray, np.ndarray]:
+    """(out, v): v = x + residual, out = v / sqrt(mean(v^2) + eps) * weight over the last axis."""
+    v = _f64(x) if residual is None else _f64(x) + _f64(residual)
+    out = v / np.sqrt((v * v).mean(-1, keepdims=True) + eps)
+    return (out if weight is None else out * _f64(weight)), v
+
+
+def row_codes(t) -> Tuple[np.ndarray, np.ndarray]:
+    """(q, m) of rows t: m = max |t|, q = nearest integer to 127 t / m, ties to even; a row of zeros
+    or with a value that is not finite has q = 0 (m = 0, or NaN)."""
+    t = _f64(t)
+    m = np.abs(t).max(-1)
+    m = np.where(np.isfinite(t).all(-1), m, np.nan)
+    ok = m > 0
+    safe = np.where(ok, m, 1.0)[..., None]
+    q = np.where(ok[..., None], np.rint(np.where(ok[..., None], t, 0.0) * 127.0 / safe), 0.0)
+    return q.astype(np.int64), m
+
+
+def rms_norm_i8(x, residual=None, weight=None, eps: float = 1e-6):
+    """(q, scale, v) of the norm's output in 8-bit codes; q * scale is the output to half a step."""
+    v = rms_norm(x, residual, None, eps)[1]
+    q, m = row_codes(v if weight is None else v * _f64(weight))
+    return q, m / 127.0 / np.sqrt((v * v).mean(-1) + eps), v
+
+
+def linear_i8(x, x_scale, w, w_scale, bias=None) -> Tuple[np.ndarray, np.ndarray]:
+    """(out, p): p = (x w^T) * x_scale * w_scale with the sum in whole numbers, out = p + bias."""
+    p = (_i64(x) @ _i64(w).T).astype(np.float64) * _f64(x_scale)[:, None] * _f64(w_scale)
+    return (p if bias is None else p + _f64(bias)), p
+
+
+def rope_angles(positions, axis_dims: Sequence[int], theta: float) -> np.ndarray:
+    """[N, d/2] angles of tokens at positions [N, 3]: frequency j of an axis of D elements is theta^(-2j/D)."""
+    pos = np.asarray(positions, dtype=np.float64)
+    cols = [pos[:, u] * theta ** (-2.0 * j / D) for u, D in enumerate(axis_dims) for j in range(D // 2)]
+    return np.stack(cols, -1)
+
+
+def rope(x, angles, halves: bool) -> np.ndarray:
+    """Pairs of the last axis of x [..., N, d] turned by angles [N, d/2] (NaN: the token is left as it is)."""
+    x = _f64(x)
+    d = x.shape[-1]
+    a, b = (x[..., :d // 2], x[..., d // 2:]) if halves else (x[..., 0::2], x[..., 1::2])
+    still = np.isnan(angles)
+    ang = np.where(still, 0.0, angles)
+    ra = np.where(still, a, a * np.cos(ang) - b * np.sin(ang))
+    rb = np.where(still, b, a * np.sin(ang) + b * np.cos(ang))
+    out = np.empty_like(x)
+    if halves:
+        out[..., :d // 2], out[..., d // 2:] = ra, rb
+    else:
+        out[..., 0::2], out[..., 1::2] = ra, rb
+    return out

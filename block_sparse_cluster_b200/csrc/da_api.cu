@@ -490,7 +490,9 @@ da_status da_linear_i8(int B, int N, int H, int d, int K, const int8_t* x, int64
     return DA_ERR_INVALID_ARG;
   const LinearArgs a{x, w, x_scale, w_scale, bias, out, M, (int)channels, K, d, N,
                      x_stride, w_stride, out_strides->batch, out_strides->head, out_strides->token};
-  return cuda_status(launch_linear_i8_simt(out_dtype == DA_BF16, a, reinterpret_cast<cudaStream_t>(stream)));
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  return cuda_status(linear_i8_tc_supported(a) ? launch_linear_i8_tc(out_dtype == DA_BF16, a, static_cast<int*>(ws), s)
+                                               : launch_linear_i8_simt(out_dtype == DA_BF16, a, s));
 }
 
 da_status da_rope(const da_rope_plan* plan, int B, int H, int N, int d, da_dtype dtype, const void* x,

@@ -93,6 +93,10 @@ struct LinearArgs {
 };
 cudaError_t launch_linear_i8_simt(bool bf16, const LinearArgs& a, cudaStream_t s);
 
+// linear_i8_tc.cu
+bool linear_i8_tc_supported(const LinearArgs& a);   // rows of x and w that TMA can read
+cudaError_t launch_linear_i8_tc(bool bf16, const LinearArgs& a, int* status, cudaStream_t s);
+
 // simt_f32.cu / simt_bf16.cu
 #define DA_SIMT_DECL(SUFFIX)                                                                                 \
   cudaError_t launch_assign_simt_##SUFFIX(const Dims& g, const void* K, const void* cent, int32_t* assign,    \

@@ -1,0 +1,426 @@
+// Product of 8-bit integer matrices with scales per token and channel, on the tensor cores.
+//
+//   out[m, n] = (sum_k x[m, k] w[n, k]) sx[m] sw[n] + bias[n]
+// tcgen05.mma kind::i8 sums in 32-bit integers in tensor memory, so the sum is exact; the epilogue
+// converts it, applies both scales and the bias in fp32 and rounds once to the output's type.
+//
+// A persistent grid walks output tiles.  Roles of a CTA (256 threads):
+//   warp 0     lane 0 loads 128-byte slices of the x and w rows by TMA into a ring of stages (128-byte
+//              swizzle; rows and depth beyond the matrices read as zero);
+//   warp 1     lane 0 issues the products of a stage (four k = 32 steps) into one of two accumulators;
+//   warp 2     allocates tensor memory;
+//   warps 4-7  epilogue: accumulator -> scaled rows -> shared memory -> 16-byte stores of whole row segments
+//              (the matrix, or the attention's heads: the segment's address is formed from its token and
+//              head), while the next tile's products fill the other accumulator.
+//
+// Two forms.  Pair (kPair): two CTAs of a cluster form a 256 x 256 tile with cta_group::2; each loads its
+// own 128 rows of x and half of the w rows, so every loaded byte serves 256 rows or columns.  Single:
+// one CTA forms 128 x kN.
+#include "da_common.cuh"
+#include "da_internal.h"
+#include "tma_host.h"
+
+namespace da {
+
+namespace {
+
+constexpr int kBlockK = 128;                 // bytes (= elements) of depth per stage
+constexpr int kTileM = 128;                  // rows of x per CTA
+constexpr int kThreads = 256;
+constexpr int kABytes = kTileM * kBlockK;    // 16 KB
+constexpr int kGroupM = 8;                   // row tiles that are walked together for each column tile
+
+template <bool kPair, int kN>
+struct Cfg {
+  static constexpr int kBRows = kPair ? kN / 2 : kN;      // w rows a CTA loads
+  static constexpr int kStageBytes = kABytes + kBRows * kBlockK;
+  static constexpr int kStages = kStageBytes >= 32768 ? 6 : 8;
+  static constexpr int kColumns = 2 * kN < 32 ? 32 : 2 * kN;   // tensor memory of two accumulators
+  static constexpr size_t kSmem = 1024 + (size_t)kStages * kStageBytes + 4 * 4096 /*staging*/ + 2 * 2 * kN * 4 /*scales, bias*/;
+};
+
+struct Params {
+  LinearArgs a;
+  int tiles_m, tiles_n, k_blocks, a_box_rows;
+  int vec;        // rows of the output can be stored 16 bytes at a time
+  int* status;
+};
+
+template <int kStages>
+struct __align__(8) Bars {
+  uint64_t full[kStages], empty[kStages];
+  uint64_t acc_full[2], acc_empty[2];
+  uint64_t drain;
+  uint32_t tmem_base;
+  int abort;
+};
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ uint32_t map_to_rank(uint32_t addr, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void arrive_at(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+
+template <bool kPair>
+__device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, uint32_t bar, int x, int y) {
+  if (kPair)
+    asm volatile("cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+                 " [%0], [%1, {%3, %4}], [%2];" ::"r"(smem_u32(dst)),
+                 "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y)
+                 : "memory");
+  else
+    asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+                 " [%0], [%1, {%3, %4}], [%2];" ::"r"(smem_u32(dst)),
+                 "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y)
+                 : "memory");
+}
+
+// D (+)= A B^T, signed 8-bit operands from shared memory, 32-bit integer sums
+template <bool kPair>
+__device__ __forceinline__ void mma_i8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  if (kPair)
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                 "tcgen05.mma.cta_group::2.kind::i8 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+                 "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+                 : "memory");
+  else
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                 "tcgen05.mma.cta_group::1.kind::i8 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+                 "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+                 : "memory");
+}
+// Arrive on `bar` (in both CTAs of a pair) when the products issued so far are done.
+template <bool kPair>
+__device__ __forceinline__ void mma_commit(uint64_t* bar) {
+  if (kPair)
+    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+                     smem_u32(bar)),
+                 "h"((uint16_t)3)
+                 : "memory");
+  else
+    umma_commit(bar);
+}
+template <bool kPair>
+__device__ __forceinline__ void alloc_columns(uint32_t* dst, uint32_t n) {
+  if (kPair) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(dst)), "r"(n) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  } else {
+    tmem_alloc(dst, n);
+    tmem_relinquish();
+  }
+}
+template <bool kPair>
+__device__ __forceinline__ void free_columns(uint32_t t, uint32_t n) {
+  if (kPair)
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(t), "r"(n) : "memory");
+  else
+    tmem_dealloc(t, n);
+}
+
+// Instruction descriptor: 32-bit integer result, signed 8-bit operands, both K-major.
+__host__ __device__ constexpr uint32_t idesc_i8(int M, int N) {
+  return (2u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+
+// Tile t of the walk: groups of kGroupM row tiles, column by column, so that the rows of x and w that the
+// resident CTAs read at one time stay in L2.
+__device__ __forceinline__ void tile_at(int t, const Params& p, int& tm, int& tn) {
+  const int per_group = kGroupM * p.tiles_n;
+  const int g = t / per_group, r = t - g * per_group;
+  const int rows = min(kGroupM, p.tiles_m - g * kGroupM);
+  tn = r / rows;
+  tm = g * kGroupM + r - tn * rows;
+}
+
+__device__ __forceinline__ void epilogue_barrier() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+
+template <typename T, bool kPair, int kN>
+__global__ void __launch_bounds__(kThreads, 1)
+linear_i8_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w,
+                    const __grid_constant__ Params p) {
+  using C = Cfg<kPair, kN>;
+  constexpr int kStages = C::kStages;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ Bars<kStages> bars;
+  const uint32_t raw = smem_u32(smem_raw);
+  uint8_t* ring = smem_raw + (((raw + 1023u) & ~1023u) - raw);
+  uint8_t* staging = ring + (size_t)kStages * C::kStageBytes;
+  float* s_cols = reinterpret_cast<float*>(staging + 4 * 4096);   // [2 tiles][scale, bias][kN]
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = kPair ? cluster_rank() : 0;
+  const int first = kPair ? blockIdx.x >> 1 : blockIdx.x;
+  const int step = kPair ? gridDim.x >> 1 : gridDim.x;
+  const int tiles = p.tiles_m * p.tiles_n;
+  constexpr int kRowsPerTile = kPair ? 2 * kTileM : kTileM;
+  volatile int* abort = &bars.abort;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(&bars.full[s], 1);
+      mbar_init(&bars.empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&bars.acc_full[b], 1);
+      mbar_init(&bars.acc_empty[b], kPair ? 8 : 4);     // one arrival per epilogue warp
+    }
+    mbar_init(&bars.drain, 1);
+    bars.abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == 2) alloc_columns<kPair>(&bars.tmem_base, C::kColumns);
+  tc_fence_before();
+  __syncthreads();
+  if (kPair) cluster_sync();
+  tc_fence_after();
+  const uint32_t tmem = bars.tmem_base;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      tma_prefetch(&tm_x);
+      tma_prefetch(&tm_w);
+      const uint32_t bytes = (uint32_t)(p.a_box_rows * kBlockK + C::kBRows * kBlockK) * (kPair ? 2u : 1u);
+      int it = 0;
+      bool ok = true;
+      for (int t = first; t < tiles && ok; t += step) {
+        int tm, tn;
+        tile_at(t, p, tm, tn);
+        const int row = tm * kRowsPerTile + (int)rank * kTileM;
+        const int col = tn * kN + (int)rank * C::kBRows;
+        for (int kb = 0; kb < p.k_blocks; ++kb, ++it) {
+          const int s = it % kStages, ph = (it / kStages) & 1;
+          if (!mbar_wait(&bars.empty[s], ph ^ 1, abort, p.status)) { ok = false; break; }
+          uint8_t* a = ring + (size_t)s * C::kStageBytes;
+          // a pair's copies all land on the leader's barrier, which expects the bytes of both
+          const uint32_t bar = kPair ? map_to_rank(smem_u32(&bars.full[s]), 0) : smem_u32(&bars.full[s]);
+          if (rank == 0) mbar_expect_tx(&bars.full[s], bytes);
+          tma_load_2d<kPair>(a, &tm_x, bar, kb * kBlockK, row);
+          tma_load_2d<kPair>(a + kABytes, &tm_w, bar, kb * kBlockK, col);
+        }
+      }
+      // given up: wait (within a limit) for the copies in flight before the block's memory goes
+      if (!ok && rank == 0)
+        for (int i = max(0, it - kStages); i < it; ++i) mbar_wait_drain(&bars.full[i % kStages], (i / kStages) & 1);
+    }
+  } else if (warp == 1 && rank == 0) {
+    if (lane == 0) {
+      const uint32_t idesc = idesc_i8(kRowsPerTile, kN);
+      int it = 0, n = 0;
+      bool ok = true;
+      for (int t = first; t < tiles && ok; t += step, ++n) {
+        const int b = n & 1;
+        if (!mbar_wait(&bars.acc_empty[b], ((n >> 1) & 1) ^ 1, abort, p.status)) break;
+        tc_fence_after();
+        for (int kb = 0; kb < p.k_blocks; ++kb, ++it) {
+          const int s = it % kStages, ph = (it / kStages) & 1;
+          if (!mbar_wait(&bars.full[s], ph, abort, p.status)) { ok = false; break; }
+          tc_fence_after();
+          const uint32_t a = smem_u32(ring + (size_t)s * C::kStageBytes);
+#pragma unroll
+          for (int ks = 0; ks < kBlockK / 32; ++ks)
+            mma_i8<kPair>(tmem + b * kN, sdesc_sw128(a + ks * 32, 16, 1024), sdesc_sw128(a + kABytes + ks * 32, 16, 1024),
+                          idesc, (kb | ks) != 0);
+          mma_commit<kPair>(&bars.empty[s]);
+        }
+        if (ok) mma_commit<kPair>(&bars.acc_full[b]);
+      }
+      if (*abort) {   // products in flight end before the tensor memory is freed
+        mma_commit<kPair>(&bars.drain);
+        mbar_wait_drain(&bars.drain, 0);
+      }
+    }
+  } else if (warp >= 4) {
+    const int ew = warp & 3;
+    uint8_t* stage = staging + ew * 4096;
+    const LinearArgs& A = p.a;
+    constexpr int kV = 16 / (int)sizeof(T);          // elements of a 16-byte store
+    constexpr int kFlush = 128 / (int)sizeof(T);     // columns of a staged row
+    const uint32_t empty0 = kPair ? map_to_rank(smem_u32(&bars.acc_empty[0]), 0) : 0;
+    int n = 0;
+    bool ok = true;   // after a wait that gave up the loop still runs, so that the four warps' barriers match
+    for (int t = first; t < tiles; t += step, ++n) {
+      int tm, tn;
+      tile_at(t, p, tm, tn);
+      const int b = n & 1;
+      const int n0 = tn * kN;
+      float* cs = s_cols + b * 2 * kN;
+      for (int i = threadIdx.x - 128; i < kN; i += 128) {
+        const bool in = n0 + i < A.N;
+        cs[i] = in ? A.w_scale[n0 + i] : 0.f;
+        cs[kN + i] = in && A.bias ? A.bias[n0 + i] : 0.f;
+      }
+      const long long m = (long long)tm * kRowsPerTile + (int)rank * kTileM + ew * 32 + lane;
+      const float sx = m < A.M ? A.x_scale[m] : 0.f;
+      const long long off = (m / A.tokens) * A.out_batch + (m % A.tokens) * A.out_token;
+      const int valid = (int)min(32LL, max(0LL, A.M - (m - lane)));   // rows of this warp inside the matrix
+      epilogue_barrier();
+      ok = __all_sync(0xffffffffu, ok && mbar_wait(&bars.acc_full[b], (n >> 1) & 1, abort, p.status));
+      if (!ok) continue;
+      tc_fence_after();
+#pragma unroll 1
+      for (int c0 = 0; c0 < kN; c0 += kFlush < kN ? kFlush : kN) {
+        constexpr int kPart = (kFlush < kN ? kFlush : kN) / 32;
+#pragma unroll
+        for (int q = 0; q < kPart; ++q) {
+          uint32_t r[32];
+          tmem_ld32(tmem + ((uint32_t)(ew * 32) << 16) + b * kN + c0 + 32 * q, r);
+          tmem_wait_ld_into(r);
+          const float4* sw4 = reinterpret_cast<const float4*>(cs + c0 + 32 * q);
+          const float4* bi4 = reinterpret_cast<const float4*>(cs + kN + c0 + 32 * q);
+          float v[32];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const float4 w = sw4[i], bi = bi4[i];
+            v[4 * i] = fmaf((float)(int)r[4 * i] * sx, w.x, bi.x);
+            v[4 * i + 1] = fmaf((float)(int)r[4 * i + 1] * sx, w.y, bi.y);
+            v[4 * i + 2] = fmaf((float)(int)r[4 * i + 2] * sx, w.z, bi.z);
+            v[4 * i + 3] = fmaf((float)(int)r[4 * i + 3] * sx, w.w, bi.w);
+          }
+          // row `lane`, 16-byte chunk j at chunk j ^ (row & 7): neither side of the transposition conflicts
+#pragma unroll
+          for (int j = 0; j < 32 / kV; ++j) {
+            const int chunk = (q * 32 / kV + j) ^ (lane & 7);
+            uint4 o;
+            if (sizeof(T) == 2)
+              o = make_uint4(pack_bf16x2(v[8 * j], v[8 * j + 1]), pack_bf16x2(v[8 * j + 2], v[8 * j + 3]),
+                             pack_bf16x2(v[(8 * j + 4) % 32], v[(8 * j + 5) % 32]), pack_bf16x2(v[(8 * j + 6) % 32], v[(8 * j + 7) % 32]));
+            else
+              o = make_uint4(__float_as_uint(v[(4 * j) % 32]), __float_as_uint(v[(4 * j + 1) % 32]),
+                             __float_as_uint(v[(4 * j + 2) % 32]), __float_as_uint(v[(4 * j + 3) % 32]));
+            *reinterpret_cast<uint4*>(stage + lane * 128 + chunk * 16) = o;
+          }
+        }
+        __syncwarp();
+        // store: 8 lanes per row segment of 128 bytes, 4 rows at a time
+        const int c = n0 + c0 + (lane & 7) * kV;
+        const bool in_part = (lane & 7) * kV < kPart * 32;
+        const long long head = (long long)(c / A.d) * A.out_head + c % A.d;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int row = i * 4 + (lane >> 3);
+          const long long ro = __shfl_sync(0xffffffffu, off, row);
+          const uint4 o = *reinterpret_cast<const uint4*>(stage + row * 128 + (((lane & 7) ^ (row & 7)) * 16));
+          if (row < valid && in_part && c < A.N) {
+            if (p.vec && c + kV <= A.N) {
+              *reinterpret_cast<uint4*>(static_cast<T*>(A.out) + ro + head) = o;
+            } else {
+              const T* e = reinterpret_cast<const T*>(&o);
+#pragma unroll
+              for (int k = 0; k < kV; ++k)
+                if (c + k < A.N)
+                  static_cast<T*>(A.out)[ro + (long long)((c + k) / A.d) * A.out_head + (c + k) % A.d] = e[k];
+            }
+          }
+        }
+        __syncwarp();
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if (kPair) arrive_at(empty0 + b * 8);
+        else mbar_arrive(&bars.acc_empty[b]);
+      }
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (kPair) cluster_sync();   // neither CTA's barriers or tensor memory go while the other may still reach them
+  if (warp == 2) {
+    tc_fence_after();
+    free_columns<kPair>(tmem, C::kColumns);
+  }
+}
+
+bool make_tmap_i8(CUtensorMap* m, const void* ptr, uint64_t K, uint64_t rows, uint64_t stride, uint32_t box_rows) {
+  EncodeTiledFn fn = get_encode_tiled();
+  if (!fn) return false;
+  cuuint64_t dims[2] = {K, rows};
+  cuuint64_t strides[1] = {stride};
+  cuuint32_t box[2] = {kBlockK, box_rows};
+  cuuint32_t estr[2] = {1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(ptr), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <typename T, bool kPair, int kN>
+cudaError_t launch_tile(const LinearArgs& a, int sms, int* status, cudaStream_t s) {
+  using C = Cfg<kPair, kN>;
+  static_assert(C::kSmem + 1024 <= 232448, "shared memory of one CTA per SM");
+  Params p;
+  p.a = a;
+  p.status = status;
+  p.tiles_m = (int)((a.M + (kPair ? 255 : 127)) / (kPair ? 256 : 128));
+  p.tiles_n = (a.N + kN - 1) / kN;
+  p.k_blocks = (a.K + kBlockK - 1) / kBlockK;
+  // rows of x beyond a short matrix are not even zeroed: their products land in rows that are not stored
+  p.a_box_rows = a.M >= kTileM || kPair ? kTileM : ((int)a.M + 7) / 8 * 8;
+  const int esz = (int)sizeof(T), v = 16 / esz;
+  p.vec = reinterpret_cast<uintptr_t>(a.out) % 16 == 0 && a.out_batch % v == 0 && a.out_token % v == 0 &&
+          (a.d == a.N || (a.d % v == 0 && a.out_head % v == 0));
+  // rows are at least their depth apart (the dispatch sees to it), one row may have any stride
+  const uint64_t xs = a.M > 1 ? a.x_stride : (a.K + 15) / 16 * 16, ws = a.N > 1 ? a.w_stride : (a.K + 15) / 16 * 16;
+  CUtensorMap tx, tw;
+  if (!make_tmap_i8(&tx, a.x, a.K, a.M, xs, p.a_box_rows)) return cudaErrorInvalidValue;
+  if (!make_tmap_i8(&tw, a.w, a.K, a.N, ws, C::kBRows)) return cudaErrorInvalidValue;
+  auto kernel = linear_i8_tc_kernel<T, kPair, kN>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem);
+  if (e != cudaSuccess) return e;
+  const long long tiles = (long long)p.tiles_m * p.tiles_n;
+  if (tiles >= (1LL << 30)) return cudaErrorInvalidValue;
+  cudaLaunchConfig_t cfg{};
+  const int slots = kPair ? sms / 2 : sms;
+  cfg.gridDim = dim3((unsigned)(tiles < slots ? tiles : slots) * (kPair ? 2 : 1));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = C::kSmem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = kPair ? 2 : 1;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, tx, tw, p);
+}
+
+template <typename T>
+cudaError_t launch_typed(const LinearArgs& a, int* status, cudaStream_t s) {
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return e;
+  const long long rows = (a.M + 127) / 128;
+  if (((a.M + 255) / 256) * ((a.N + 255) / 256) >= sms / 2) return launch_tile<T, true, 256>(a, sms, status, s);
+  if (rows * ((a.N + 127) / 128) >= sms) return launch_tile<T, false, 128>(a, sms, status, s);
+  if (rows * ((a.N + 63) / 64) >= sms) return launch_tile<T, false, 64>(a, sms, status, s);
+  return launch_tile<T, false, 32>(a, sms, status, s);
+}
+
+}  // namespace
+
+bool linear_i8_tc_supported(const LinearArgs& a) {
+  auto rows_ok = [&](const void* p, long long rows, long long stride) {
+    return reinterpret_cast<uintptr_t>(p) % 16 == 0 && (rows == 1 || (stride % 16 == 0 && stride >= a.K && stride < (1LL << 40)));
+  };
+  // tile rows are 32-bit coordinates
+  return a.M < (1LL << 31) - 256 && rows_ok(a.x, a.M, a.x_stride) && rows_ok(a.w, a.N, a.w_stride);
+}
+
+cudaError_t launch_linear_i8_tc(bool bf16, const LinearArgs& a, int* status, cudaStream_t s) {
+  return bf16 ? launch_typed<__nv_bfloat16>(a, status, s) : launch_typed<float>(a, status, s);
+}
+
+}  // namespace da

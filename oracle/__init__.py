@@ -370,7 +370,8 @@ def rms_norm_i8(x, residual=None, weight=None, eps: float = 1e-6):
 
 def linear_i8(x, x_scale, w, w_scale, bias=None) -> Tuple[np.ndarray, np.ndarray]:
     """(out, p): p = (x w^T) * x_scale * w_scale with the sum in whole numbers, out = p + bias."""
-    p = (_i64(x) @ _i64(w).T).astype(np.float64) * _f64(x_scale)[:, None] * _f64(w_scale)
+    # whole numbers below 2^53: fp64 sums them exactly
+    p = (_f64(x) @ _f64(w).T) * _f64(x_scale)[:, None] * _f64(w_scale)
     return (p if bias is None else p + _f64(bias)), p
 
 

@@ -262,6 +262,24 @@ def test_linear_into_heads(B, H, N, d, K, dtype):
     assert (heads[:, H:] == 7).all() and (heads[:, :, N:] == 7).all() and da.da_device_status(ws) == 0
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("M,C,K", [(2500, 2000, 272), (18900, 250, 1600), (4864, 1024, 128), (1100, 4096, 640)])
+def test_linear_over_many_tiles(M, C, K, dtype):
+    """Products of more tiles than the GPU has processors, ragged on every side; heads on the last."""
+    x, w = _codes(M, K, K, 1), _codes(C, K, K, 2)
+    sx, sw, bias = _scales(M, 3), _scales(C, 4), torch.randn(C, generator=_gen(6))
+    ws = torch.zeros(256, dtype=torch.uint8, device="cuda")
+    out = torch.full((M + 1, C + 8), 7.0, dtype=dtype, device="cuda")
+    da.da_linear_i8(x, sx.cuda(), w, sw.cuda(), out[:M, :C], ws, bias=bias.cuda())
+    assert da.da_device_status(ws) == 0
+    _linear_close(out[:M, :C], x, sx, w, sw, bias, dtype)
+    assert (out[M:] == 7).all() and (out[:, C:] == 7).all()
+    if C % 128 == 0:
+        heads = torch.full((2, C // 128, M // 2, 128), 7.0, dtype=dtype, device="cuda")
+        da.da_linear_i8(x, sx.cuda(), w, sw.cuda(), heads, ws, bias=bias.cuda())
+        assert torch.equal(heads.permute(0, 2, 1, 3).reshape(M, C), out[:M, :C])
+
+
 def test_linear_extremes():
     """The largest sums (every code -128 at the deepest product), codes of a row that was not finite, zero scales."""
     K = 131071

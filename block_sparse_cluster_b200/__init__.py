@@ -332,64 +332,79 @@ _CODES = {torch.bfloat16: DA_BF16, torch.float32: DA_F32}
 _INVALID_ARG, _SHAPE, _DTYPE = 1, 2, 3
 
 
-def _same_place(where: str, *tensors: Optional[torch.Tensor]) -> torch.device:
+def _refuse(code: int, where: str, what: str):
+    raise DAError(code, f"{where}: {what}")
+
+
+def _device(where: str, *tensors: Optional[torch.Tensor]) -> int:
     """The one CUDA device that holds all the tensors."""
-    device = tensors[0].device
+    device = tensors[0].get_device()
     for t in tensors:
-        if t is not None and (t.device != device or t.device.type != "cuda"):
-            raise DAError(_INVALID_ARG, f"{where}: tensors have to be on one CUDA device")
+        if t is not None and (t.get_device() != device or device < 0):
+            _refuse(_INVALID_ARG, where, "tensors have to be on one CUDA device")
     return device
-
-
-def _need(ok: bool, code: int, where: str, what: str):
-    if not ok:
-        raise DAError(code, f"{where}: {what}")
 
 
 def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
     return None if t is None else t.data_ptr()
 
 
-def _rows(t: Optional[torch.Tensor], shape, dtype, where: str, what: str) -> int:
-    """The row stride of a [rows, width] tensor with contiguous rows (0 for None)."""
-    if t is None:
-        return 0
-    _need(tuple(t.shape) == tuple(shape), _SHAPE, where, f"{what} has to be {list(shape)}")
-    _need(t.dtype == dtype, _DTYPE, where, f"{what} has to be {dtype}")
-    _need(t.stride(1) == 1 or t.shape[1] == 1, _SHAPE, where, f"{what} needs contiguous rows")
-    return t.stride(0) if t.shape[0] > 1 else max(t.shape[1], t.stride(0))
+def _code(t: torch.Tensor, where: str, what: str) -> int:
+    if t.dtype not in _CODES:
+        _refuse(_DTYPE, where, what + " has to be bfloat16 or float32")
+    return _CODES[t.dtype]
 
 
-def _vector(t: Optional[torch.Tensor], n: int, dtype, where: str, what: str):
-    if t is not None:
-        _need(t.dim() == 1 and t.shape[0] == n, _SHAPE, where, f"{what} has to be [{n}]")
-        _need(t.dtype == dtype, _DTYPE, where, f"{what} has to be {dtype}")
-        _need(n == 1 or t.stride(0) == 1, _SHAPE, where, f"{what} has to be contiguous")
+def _rows(t: torch.Tensor, rows: int, width: int, dtype, where: str, what: str) -> int:
+    """The row stride of a [rows, width] tensor with contiguous rows."""
+    if t.shape != (rows, width):
+        _refuse(_SHAPE, where, f"{what} has to be [{rows}, {width}]")
+    if t.dtype != dtype:
+        _refuse(_DTYPE, where, f"{what} has to be {dtype}")
+    stride, inner = t.stride()
+    if inner != 1 and width > 1:
+        _refuse(_SHAPE, where, f"{what} needs contiguous rows")
+    return stride if rows > 1 else max(width, stride)
+
+
+def _vector(t: torch.Tensor, n: int, dtype, where: str, what: str):
+    if t.shape != (n,):
+        _refuse(_SHAPE, where, f"{what} has to be [{n}]")
+    if t.dtype != dtype:
+        _refuse(_DTYPE, where, f"{what} has to be {dtype}")
+    if n > 1 and t.stride(0) != 1:
+        _refuse(_SHAPE, where, f"{what} has to be contiguous")
 
 
 def _head_strides(t: torch.Tensor, where: str, what: str) -> _HeadStrides:
     """Strides of a [B, H, N, d] tensor with contiguous heads."""
-    _need(t.dim() == 4, _SHAPE, where, f"{what} has to be [B, H, N, d]")
-    _need(t.stride(3) == 1 or t.shape[3] == 1, _SHAPE, where, f"{what} needs a contiguous last dimension")
-    return _HeadStrides(t.stride(0), t.stride(1), t.stride(2))
+    if t.dim() != 4:
+        _refuse(_SHAPE, where, f"{what} has to be [B, H, N, d]")
+    batch, head, token, inner = t.stride()
+    if inner != 1 and t.shape[3] > 1:
+        _refuse(_SHAPE, where, f"{what} needs a contiguous last dimension")
+    return _HeadStrides(batch, head, token)
 
 
-def _on(device: torch.device, stream, f, *args) -> int:
-    """Calls f(*args, stream) with `device` current."""
-    if device.index == torch.cuda.current_device():
-        return f(*args, _stream(stream))
+def _on(device: int, stream, f, *args) -> int:
+    """f(*args, stream) with `device` current; the stream is the device's current one by default."""
+    raw = torch._C._cuda_getCurrentRawStream(device) if stream is None else _stream(stream)
+    if device == torch.cuda.current_device():
+        return f(*args, raw)
     with torch.cuda.device(device):
-        return f(*args, _stream(stream))
+        return f(*args, raw)
 
 
 def _norm_args(where, x, weight, residual, sum_out, eps):
-    _need(x.dim() == 2, _SHAPE, where, "x has to be [rows, width]")
-    _need(x.dtype in _CODES, _DTYPE, where, "x has to be bfloat16 or float32")
+    code = _code(x, where, "x")
+    if x.dim() != 2:
+        _refuse(_SHAPE, where, "x has to be [rows, width]")
     rows, width = x.shape
-    _vector(weight, width, x.dtype, where, "weight")
-    return (rows, width, _CODES[x.dtype], x.data_ptr(), _rows(x, x.shape, x.dtype, where, "x"), _ptr(residual),
-            _rows(residual, x.shape, x.dtype, where, "residual"), _ptr(weight), float(eps), _ptr(sum_out),
-            _rows(sum_out, x.shape, x.dtype, where, "sum_out"))
+    if weight is not None:
+        _vector(weight, width, x.dtype, where, "weight")
+    return (rows, width, code, x.data_ptr(), _rows(x, rows, width, x.dtype, where, "x"), _ptr(residual),
+            0 if residual is None else _rows(residual, rows, width, x.dtype, where, "residual"), _ptr(weight), eps,
+            _ptr(sum_out), 0 if sum_out is None else _rows(sum_out, rows, width, x.dtype, where, "sum_out"))
 
 
 def da_rms_norm(x: torch.Tensor, weight: Optional[torch.Tensor], out: torch.Tensor,
@@ -398,9 +413,9 @@ def da_rms_norm(x: torch.Tensor, weight: Optional[torch.Tensor], out: torch.Tens
     """out = v / sqrt(mean(v^2) + eps) * weight with v = x + residual, rows [rows, width] of bf16 or
     fp32; sum_out takes v (the residual stream; it may be the residual's or x's own buffer)."""
     where = "da_rms_norm"
-    device = _same_place(where, x, weight, out, residual, sum_out)
+    device = _device(where, x, weight, out, residual, sum_out)
     _check(_on(device, stream, _lib.da_rms_norm, *_norm_args(where, x, weight, residual, sum_out, eps), out.data_ptr(),
-               _rows(out, x.shape, x.dtype, where, "out")), where)
+               _rows(out, x.shape[0], x.shape[1], x.dtype, where, "out")), where)
     return out
 
 
@@ -410,11 +425,11 @@ def da_rms_norm_i8(x: torch.Tensor, weight: Optional[torch.Tensor], q: torch.Ten
     """da_rms_norm with its output in 8-bit codes: q [rows, width] int8 (rows may be padded: a row
     stride that is a multiple of 16 suits da_linear_i8), scale [rows] fp32, output = q * scale."""
     where = "da_rms_norm_i8"
-    device = _same_place(where, x, weight, q, scale, residual, sum_out)
+    device = _device(where, x, weight, q, scale, residual, sum_out)
     args = _norm_args(where, x, weight, residual, sum_out, eps)
     _vector(scale, x.shape[0], torch.float32, where, "scale")
-    _check(_on(device, stream, _lib.da_rms_norm_i8, *args, q.data_ptr(), _rows(q, x.shape, torch.int8, where, "q"),
-               scale.data_ptr()), where)
+    _check(_on(device, stream, _lib.da_rms_norm_i8, *args, q.data_ptr(),
+               _rows(q, x.shape[0], x.shape[1], torch.int8, where, "q"), scale.data_ptr()), where)
     return q, scale
 
 
@@ -422,17 +437,17 @@ def da_quantize_i8(x: torch.Tensor, q: torch.Tensor, scale: torch.Tensor, stream
     """Rows in 8-bit codes with a scale each, x ~ q * scale: x is [rows, width], or the attention's
     [B, H, N, d], whose token (b, n) becomes row b * N + n of q [B*N, H*d] (heads side by side)."""
     where = "da_quantize_i8"
-    device = _same_place(where, x, q, scale)
-    _need(x.dtype in _CODES, _DTYPE, where, "x has to be bfloat16 or float32")
+    device = _device(where, x, q, scale)
+    code = _code(x, where, "x")
     if x.dim() == 2:
-        strides = _HeadStrides(0, 0, _rows(x, x.shape, x.dtype, where, "x"))
-        B, H, N, d = 1, 1, x.shape[0], x.shape[1]
+        B, H, (N, d) = 1, 1, x.shape
+        strides = _HeadStrides(0, 0, _rows(x, N, d, x.dtype, where, "x"))
     else:
         strides = _head_strides(x, where, "x")
         B, H, N, d = x.shape
     _vector(scale, B * N, torch.float32, where, "scale")
-    _check(_on(device, stream, _lib.da_quantize_i8, B, H, N, d, _CODES[x.dtype], x.data_ptr(), ctypes.byref(strides),
-               q.data_ptr(), _rows(q, (B * N, H * d), torch.int8, where, "q"), scale.data_ptr()), where)
+    _check(_on(device, stream, _lib.da_quantize_i8, B, H, N, d, code, x.data_ptr(), ctypes.byref(strides),
+               q.data_ptr(), _rows(q, B * N, H * d, torch.int8, where, "q"), scale.data_ptr()), where)
     return q, scale
 
 
@@ -442,23 +457,28 @@ def da_linear_i8(x: torch.Tensor, x_scale: torch.Tensor, w: torch.Tensor, w_scal
     and [C], fp32 bias [C]; out is [M, C] or, as heads, [B, H, N, d] with B*N = M, H*d = C, of bf16 or
     fp32.  ws: a zero-filled workspace of at least 256 bytes (one of `workspace(dims)` serves too)."""
     where = "da_linear_i8"
-    device = _same_place(where, x, x_scale, w, w_scale, out, ws, bias)
-    _need(out.dtype in _CODES, _DTYPE, where, "out has to be bfloat16 or float32")
-    _need(x.dim() == 2 and w.dim() == 2, _SHAPE, where, "x and w have to be matrices")
+    device = _device(where, x, x_scale, w, w_scale, out, ws, bias)
+    code = _code(out, where, "out")
+    if x.dim() != 2 or w.dim() != 2:
+        _refuse(_SHAPE, where, "x and w have to be matrices")
     (M, K), C = x.shape, w.shape[0]
     if out.dim() == 2:
-        strides = _HeadStrides(0, 0, _rows(out, (M, C), out.dtype, where, "out"))
         B, H, N, d = 1, 1, M, C
+        strides = _HeadStrides(0, 0, _rows(out, M, C, out.dtype, where, "out"))
     else:
         strides = _head_strides(out, where, "out")
         B, H, N, d = out.shape
-        _need(B * N == M and H * d == C, _SHAPE, where, f"out has to hold {M} tokens of {C} channels")
+        if B * N != M or H * d != C:
+            _refuse(_SHAPE, where, f"out has to hold {M} tokens of {C} channels")
     _vector(x_scale, M, torch.float32, where, "x_scale")
     _vector(w_scale, C, torch.float32, where, "w_scale")
-    _vector(bias, C, torch.float32, where, "bias")
-    _check(_on(device, stream, _lib.da_linear_i8, B, N, H, d, K, x.data_ptr(), _rows(x, (M, K), torch.int8, where, "x"),
-               x_scale.data_ptr(), w.data_ptr(), _rows(w, (C, K), torch.int8, where, "w"), w_scale.data_ptr(),
-               _ptr(bias), _CODES[out.dtype], out.data_ptr(), ctypes.byref(strides), ws.data_ptr(),
+    if bias is not None:
+        _vector(bias, C, torch.float32, where, "bias")
+    if not ws.is_contiguous():
+        _refuse(_SHAPE, where, "ws has to be contiguous")
+    _check(_on(device, stream, _lib.da_linear_i8, B, N, H, d, K, x.data_ptr(), _rows(x, M, K, torch.int8, where, "x"),
+               x_scale.data_ptr(), w.data_ptr(), _rows(w, C, K, torch.int8, where, "w"), w_scale.data_ptr(),
+               _ptr(bias), code, out.data_ptr(), ctypes.byref(strides), ws.data_ptr(),
                ws.numel() * ws.element_size()), where)
     return out
 
@@ -487,24 +507,27 @@ def da_rope(x: torch.Tensor, out: torch.Tensor, rope: Rope, positions: Optional[
     projection's token rows) into out, which may be x.  positions: int32 [N, 3] or [B, N, 3]; None:
     the rope's grid.  weight [d] or [H*d]: the head or the token is normed first."""
     where = "da_rope"
-    device = _same_place(where, x, out, positions, weight)
-    _need(x.dtype in _CODES, _DTYPE, where, "x has to be bfloat16 or float32")
-    _need(out.dtype == x.dtype and (weight is None or weight.dtype == x.dtype), _DTYPE, where,
-          "out and weight have to be of x's type")
+    device = _device(where, x, out, positions, weight)
+    code = _code(x, where, "x")
+    if out.dtype != x.dtype:
+        _refuse(_DTYPE, where, "out has to be of x's type")
     xs, os_ = _head_strides(x, where, "x"), _head_strides(out, where, "out")
-    _need(out.shape == x.shape, _SHAPE, where, "out has to be of x's shape")
+    if out.shape != x.shape:
+        _refuse(_SHAPE, where, "out has to be of x's shape")
     B, H, N, d = x.shape
-    batch = 0
+    batch = width = 0
     if positions is not None:
-        _need(positions.dtype == torch.int32, _DTYPE, where, "positions have to be int32")
-        _need(tuple(positions.shape) in ((N, 3), (B, N, 3)) and positions.is_contiguous(), _SHAPE, where,
-              "positions have to be contiguous [N, 3] or [B, N, 3]")
+        if positions.dtype != torch.int32:
+            _refuse(_DTYPE, where, "positions have to be int32")
+        if positions.shape not in ((N, 3), (B, N, 3)) or not positions.is_contiguous():
+            _refuse(_SHAPE, where, f"positions have to be contiguous [{N}, 3] or [{B}, {N}, 3]")
         batch = 3 * N if positions.dim() == 3 else 0
     if weight is not None:
-        _vector(weight, weight.numel(), x.dtype, where, "weight")
-    _check(_on(device, stream, _lib.da_rope, ctypes.byref(rope.c()), B, H, N, d, _CODES[x.dtype], x.data_ptr(),
-               ctypes.byref(xs), _ptr(positions), batch, _ptr(weight), 0 if weight is None else weight.numel(), float(eps),
-               out.data_ptr(), ctypes.byref(os_)), where)
+        width = weight.numel()
+        _vector(weight, width, x.dtype, where, "weight")
+    _check(_on(device, stream, _lib.da_rope, ctypes.byref(rope.c()), B, H, N, d, code, x.data_ptr(),
+               ctypes.byref(xs), _ptr(positions), batch, _ptr(weight), width, eps, out.data_ptr(),
+               ctypes.byref(os_)), where)
     return out
 
 

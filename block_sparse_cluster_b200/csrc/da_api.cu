@@ -458,7 +458,7 @@ da_status da_quantize_i8(int B, int H, int N, int d, da_dtype dtype, const void*
   const long long rows = (long long)B * N;
   const View vx = heads(x, element_size(dtype), B, H, N, d, *x_strides);
   const View vq = matrix(q, 1, rows, H * d, q_stride), vc = matrix(scale, 4, rows, 1, 1);
-  if (rows >= (1LL << 31) || !vx.fits() || !vq.fits() || !vq.distinct()) return DA_ERR_SHAPE;
+  if (B > 65535 || rows >= (1LL << 31) || !vx.fits() || !vq.fits() || !vq.distinct()) return DA_ERR_SHAPE;
   if (!vx.element_aligned() || !vc.element_aligned()) return DA_ERR_ALIGNMENT;
   if (!apart(vq, vx, false) || !apart(vq, vc, false) || !apart(vc, vx, false)) return DA_ERR_INVALID_ARG;
   return cuda_status(launch_quantize_i8(dtype == DA_BF16, B, H, N, d, x, *x_strides, q, q_stride, scale,
@@ -524,7 +524,8 @@ da_status da_rope(const da_rope_plan* plan, int B, int H, int N, int d, da_dtype
   const View vx = heads(x, size, B, H, N, d, *x_strides), vo = heads(out, size, B, H, N, d, *out_strides);
   const View vw = matrix(weight, size, 1, weight ? weight_width : 1, 0);
   const View vp = View{positions, 3, 4, {1, B, N}, {0, positions_batch, 3}};
-  if ((long long)B * N >= (1LL << 31) || !vx.fits() || !vo.fits() || !vo.distinct()) return DA_ERR_SHAPE;
+  if (B > 65535 || H > 65535 || (long long)B * N >= (1LL << 31)) return DA_ERR_SHAPE;
+  if (!vx.fits() || !vo.fits() || !vo.distinct()) return DA_ERR_SHAPE;
   if (positions && (!vp.fits() || (positions_batch != 0 && positions_batch < 3LL * N))) return DA_ERR_SHAPE;
   if (!vx.aligned16() || !vo.aligned16() || reinterpret_cast<uintptr_t>(weight) % 16 != 0 || !vp.element_aligned())
     return DA_ERR_ALIGNMENT;

@@ -7,7 +7,13 @@
 //
 // Angles are formed in fp64 in units of half turns, reduced to [-1, 1] there, and only then
 // rounded for sincospif: position times frequency loses nothing however far the position.
-// A token's d/2 angles are formed once and serve all its heads.
+//
+// The kernel is bound by HBM: x is read once and out written once.  A thread's unit of work is two
+// 16-byte vectors of a head, elements [j, j + V) and [j + d/2, j + d/2 + V): whole pairs in either pairing.
+// A group of threads owns a token, all its heads, in registers (the norm over all heads needs them
+// together); every unit of a thread has the same j, so its cosines and sines are loaded from shared memory
+// once a token.  A block takes a run of tokens: all its threads form the angles of the whole run first, behind
+// the loads of the first token, and each token's loads are issued before the one in front is worked on.
 #include <math.h>
 
 #include "da_common.cuh"
@@ -18,97 +24,242 @@ namespace da {
 namespace {
 
 constexpr int kMaxPairs = 64;   // d <= 128
+constexpr int kMaxRun = 32;     // tokens of a block
+
+enum { kNoNorm = 0, kHeadNorm = 1, kFullNorm = 2 };
 
 struct RopeArgs {
   const void* x;
   void* out;
-  const void* weight;          // or null: no norm
+  const void* weight;
   const int* positions;        // [batch][N][3], or null: the grid
   long long pos_batch;
   int H, N;
-  long long rows;              // B * N
+  int heads_per_block;         // H, or less where a token's heads are spread over blocks
+  int group;                   // threads of a token: a power of two up to 32, or the whole block
+  int run;                     // tokens of a block
   long long xb, xh, xn, ob, oh, on;
   int grid[3];
-  int full;                    // the norm runs over all heads
+  int norm, halves;
   float eps;
   double freq[kMaxPairs];      // frequency / pi: half turns per position
   unsigned char axis[kMaxPairs];
 };
 
-template <typename T, int D>
-__global__ void __launch_bounds__(128) rope_kernel(const __grid_constant__ RopeArgs a, int halves) {
-  __shared__ float s_cos[D / 2], s_sin[D / 2];
-  __shared__ float s_part[4];
-  __shared__ int s_turn;
-  const long long row = blockIdx.x;
-  const int b = (int)(row / a.N), n = (int)(row % a.N);
-  const int tid = threadIdx.x;
-  const T* x = static_cast<const T*>(a.x) + b * a.xb + n * a.xn;
-  T* out = static_cast<T*>(a.out) + b * a.ob + n * a.on;
-  if (tid < D / 2) {
-    const int u = a.axis[tid];
+template <typename T>
+struct Vec;   // 16 bytes
+template <>
+struct Vec<__nv_bfloat16> {
+  static constexpr int n = 8;
+  static __device__ __forceinline__ void unpack(const uint4& raw, float* o) {
+    const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      o[2 * i] = __uint_as_float(w[i] << 16);
+      o[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+  }
+  static __device__ __forceinline__ uint4 pack(const float* v) {
+    return make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+  }
+};
+template <>
+struct Vec<float> {
+  static constexpr int n = 4;
+  static __device__ __forceinline__ void unpack(const uint4& raw, float* o) {
+    o[0] = __uint_as_float(raw.x); o[1] = __uint_as_float(raw.y);
+    o[2] = __uint_as_float(raw.z); o[3] = __uint_as_float(raw.w);
+  }
+  static __device__ __forceinline__ uint4 pack(const float* v) {
+    return make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+  }
+};
+
+// UPT: units a thread holds of a token.
+template <typename T, int D, int UPT>
+__global__ void __launch_bounds__(512) rope_kernel(const __grid_constant__ RopeArgs a) {
+  constexpr int V = Vec<T>::n;
+  constexpr int kPerHead = D / 2 / V;   // units of a head
+  __shared__ __align__(16) float s_cos[kMaxRun * D / 2], s_sin[kMaxRun * D / 2];
+  __shared__ bool s_turn[kMaxRun];
+  __shared__ float s_part[2][16];
+  const int b = blockIdx.y, n0 = blockIdx.x * a.run, h0 = blockIdx.z * a.heads_per_block;
+  const int run = min(a.run, a.N - n0);
+  const int units = min(a.heads_per_block, a.H - h0) * kPerHead;
+  const int groups = blockDim.x / a.group;
+  const int g = threadIdx.x / a.group, gt = threadIdx.x - g * a.group;
+  const int j = (gt % kPerHead) * V;    // the same for all units of a thread: group is a multiple of kPerHead
+  const T* x = static_cast<const T*>(a.x) + b * a.xb + (long long)h0 * a.xh + j;
+  T* out = static_cast<T*>(a.out) + b * a.ob + (long long)h0 * a.oh + j;
+  const T* weight = static_cast<const T*>(a.weight) + j;
+
+  uint4 raw[UPT][2], next[UPT][2];
+  auto load = [&](int k, uint4 (&r)[UPT][2]) {
+    const T* p = x + (long long)(n0 + k) * a.xn;
+#pragma unroll
+    for (int i = 0; i < UPT; ++i) {
+      const int u = gt + i * a.group;
+      r[i][0] = r[i][1] = make_uint4(0, 0, 0, 0);
+      if (u < units && k < run) {
+        const T* e = p + (u / kPerHead) * a.xh;
+        r[i][0] = *reinterpret_cast<const uint4*>(e);
+        r[i][1] = *reinterpret_cast<const uint4*>(e + D / 2);
+      }
+    }
+  };
+  load(g, raw);
+
+  for (int i = threadIdx.x; i < run * (D / 2); i += blockDim.x) {
+    const int k = i / (D / 2), p = i % (D / 2), u = a.axis[p];
+    const unsigned n = (unsigned)(n0 + k);
     int pos;
     bool turn = true;
     if (a.positions) {
       pos = a.positions[b * a.pos_batch + (long long)n * 3 + u];
     } else {
-      const int w = n % a.grid[2], h = n / a.grid[2] % a.grid[1], t = n / a.grid[2] / a.grid[1];
-      pos = u == 0 ? t : u == 1 ? h : w;
-      turn = t < a.grid[0];
+      const unsigned row = n / (unsigned)a.grid[2], t = row / (unsigned)a.grid[1];
+      pos = (int)(u == 0 ? t : u == 1 ? row - t * a.grid[1] : n - row * a.grid[2]);
+      turn = t < (unsigned)a.grid[0];
     }
-    double half_turns = (double)pos * a.freq[tid];
+    double half_turns = (double)pos * a.freq[p];
     half_turns -= 2.0 * rint(half_turns * 0.5);
-    sincospif((float)half_turns, &s_sin[tid], &s_cos[tid]);
-    if (tid == 0) s_turn = turn;
-  }
-  const int total = a.H * D;
-  float full = 1.f;
-  if (a.weight && a.full) {
-    float ss = 0.f;
-    for (int i = tid; i < total; i += blockDim.x) {
-      const float v = to_f32(x[(i / D) * a.xh + i % D]);
-      ss = fmaf(v, v, ss);
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-    if ((tid & 31) == 0) s_part[tid >> 5] = ss;
-    __syncthreads();
-    full = rsqrtf(((s_part[0] + s_part[1]) + (s_part[2] + s_part[3])) / (float)total + a.eps);
+    sincospif((float)half_turns, &s_sin[i], &s_cos[i]);
+    if (p == 0) s_turn[k] = turn;
   }
   __syncthreads();
-  const T* w = static_cast<const T*>(a.weight);
-  // one warp per head: lane l holds pairs l, l + 32
-  for (int h = tid >> 5; h < a.H; h += 4) {
-    float va[D / 64], vb[D / 64];
-    float ss = 0.f;
+
+  // every group takes the same number of turns, so that the barriers match
+  for (int k0 = 0, it = 0; k0 < run; k0 += groups, ++it) {
+    const int k = k0 + g;
+    const bool more = k0 + groups < run;
+    if (more) load(k + groups, next);
+    float v[UPT][2][V];
+    float ss = 0.f, factor[UPT];
 #pragma unroll
-    for (int i = 0; i < D / 64; ++i) {
-      const int p = (tid & 31) + 32 * i;
-      const int ia = halves ? p : 2 * p, ib = halves ? p + D / 2 : 2 * p + 1;
-      va[i] = to_f32(x[h * a.xh + ia]);
-      vb[i] = to_f32(x[h * a.xh + ib]);
-      ss = fmaf(va[i], va[i], fmaf(vb[i], vb[i], ss));
-    }
-    float f = full;
-    if (w && !a.full) {
+    for (int i = 0; i < UPT; ++i) {
+      Vec<T>::unpack(raw[i][0], v[i][0]);
+      Vec<T>::unpack(raw[i][1], v[i][1]);
+      factor[i] = 0.f;
+      if (a.norm != kNoNorm) {
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-      f = rsqrtf(ss / (float)D + a.eps);
-    }
-#pragma unroll
-    for (int i = 0; i < D / 64; ++i) {
-      const int p = (tid & 31) + 32 * i;
-      const int ia = halves ? p : 2 * p, ib = halves ? p + D / 2 : 2 * p + 1;
-      if (w) {
-        va[i] *= f * to_f32(w[(a.full ? h * D : 0) + ia]);
-        vb[i] *= f * to_f32(w[(a.full ? h * D : 0) + ib]);
+        for (int e = 0; e < V; ++e) factor[i] = fmaf(v[i][0][e], v[i][0][e], fmaf(v[i][1][e], v[i][1][e], factor[i]));
+        ss += factor[i];
       }
-      const float c = s_cos[p], s = s_sin[p];
-      // a token that does not turn is copied, whatever it holds
-      store_out(out + h * a.oh + ia, s_turn ? va[i] * c - vb[i] * s : va[i]);
-      store_out(out + h * a.oh + ib, s_turn ? va[i] * s + vb[i] * c : vb[i]);
+    }
+    if (a.norm == kHeadNorm) {
+#pragma unroll
+      for (int i = 0; i < UPT; ++i) {
+#pragma unroll
+        for (int o = kPerHead / 2; o > 0; o >>= 1) factor[i] += __shfl_xor_sync(0xffffffffu, factor[i], o);
+        factor[i] = rsqrtf(factor[i] * (1.f / D) + a.eps);
+      }
+    } else if (a.norm == kFullNorm) {
+      for (int o = min(a.group, 32) / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+      if (a.group > 32) {
+        if ((threadIdx.x & 31) == 0) s_part[it & 1][threadIdx.x >> 5] = ss;
+        __syncthreads();
+        ss = (threadIdx.x & 31) < (blockDim.x >> 5) ? s_part[it & 1][threadIdx.x & 31] : 0.f;
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+        ss = __shfl_sync(0xffffffffu, ss, 0);
+      }
+      const float f = rsqrtf(ss / (float)(a.H * D) + a.eps);
+#pragma unroll
+      for (int i = 0; i < UPT; ++i) factor[i] = f;
+    }
+    if (k < run) {
+      T* o = out + (long long)(n0 + k) * a.on;
+      const bool turn = s_turn[k];
+      __align__(16) float c[V], s[V];   // halves: pairs j .. j + V; adjacent: V / 2 pairs of each vector
+#pragma unroll
+      for (int q = 0; q < V; q += 4) {
+        const int at = k * (D / 2) + (a.halves ? j + q : q < V / 2 ? j / 2 + q : j / 2 + D / 4 + q - V / 2);
+        if (V == 8 || a.halves) {
+          *reinterpret_cast<float4*>(&c[q]) = *reinterpret_cast<const float4*>(s_cos + at);
+          *reinterpret_cast<float4*>(&s[q]) = *reinterpret_cast<const float4*>(s_sin + at);
+        } else {   // V = 4, adjacent: two pairs of each vector
+          *reinterpret_cast<float2*>(&c[0]) = *reinterpret_cast<const float2*>(s_cos + at);
+          *reinterpret_cast<float2*>(&s[0]) = *reinterpret_cast<const float2*>(s_sin + at);
+          *reinterpret_cast<float2*>(&c[2]) = *reinterpret_cast<const float2*>(s_cos + at + D / 4);
+          *reinterpret_cast<float2*>(&s[2]) = *reinterpret_cast<const float2*>(s_sin + at + D / 4);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < UPT; ++i) {
+        const int u = gt + i * a.group;
+        if (u >= units) continue;
+        const int h = u / kPerHead;
+        if (a.norm != kNoNorm) {
+          const T* w = weight + (a.norm == kFullNorm ? h * D : 0);
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            float wv[V];
+            Vec<T>::unpack(*reinterpret_cast<const uint4*>(w + q * (D / 2)), wv);
+#pragma unroll
+            for (int e = 0; e < V; ++e) v[i][q][e] *= factor[i] * wv[e];
+          }
+        }
+        if (turn) {   // a token that does not turn is copied, whatever it holds
+          if (a.halves) {
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+              const float va = v[i][0][e], vb = v[i][1][e];
+              v[i][0][e] = va * c[e] - vb * s[e];
+              v[i][1][e] = va * s[e] + vb * c[e];
+            }
+          } else {
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+#pragma unroll
+              for (int e = 0; e < V / 2; ++e) {
+                const float va = v[i][q][2 * e], vb = v[i][q][2 * e + 1];
+                const float ce = c[q * (V / 2) + e], se = s[q * (V / 2) + e];
+                v[i][q][2 * e] = va * ce - vb * se;
+                v[i][q][2 * e + 1] = va * se + vb * ce;
+              }
+          }
+        }
+        T* e = o + (long long)h * a.oh;
+        *reinterpret_cast<uint4*>(e) = Vec<T>::pack(v[i][0]);
+        *reinterpret_cast<uint4*>(e + D / 2) = Vec<T>::pack(v[i][1]);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < UPT; ++i) {
+      raw[i][0] = next[i][0];
+      raw[i][1] = next[i][1];
     }
   }
+}
+
+template <typename T, int D>
+cudaError_t launch_typed(RopeArgs& a, int B, cudaStream_t s) {
+  constexpr int kPerHead = D / 2 / Vec<T>::n;
+  // without the norm over all heads a token's heads may go to several blocks
+  a.heads_per_block = a.norm == kFullNorm ? a.H : (a.H < 1024 / kPerHead ? a.H : 1024 / kPerHead);
+  const int units = a.heads_per_block * kPerHead;
+  int threads, upt;
+  if (units <= 128) {   // a warp, or less, a token
+    a.group = kPerHead;
+    while (a.group < units && a.group < 32) a.group *= 2;
+    upt = (units + 31) / 32;
+    threads = 128;
+  } else {
+    upt = units <= 1024 ? 2 : 4;
+    threads = a.group = ((units + upt - 1) / upt + 31) / 32 * 32;
+  }
+  const int groups = threads / a.group;
+  // run: long enough to spread the angles over the threads, short enough for the blocks to fill the GPU
+  const long long tokens = (long long)B * a.N;
+  int per_group = 1;
+  while (per_group < 8 && groups * per_group * 2 <= kMaxRun && tokens / (groups * per_group * 2) >= 148 * 16) per_group *= 2;
+  a.run = groups * per_group;
+  const dim3 grid((unsigned)((a.N + a.run - 1) / a.run), (unsigned)B, (unsigned)((a.H + a.heads_per_block - 1) / a.heads_per_block));
+  if (upt == 1) rope_kernel<T, D, 1><<<grid, threads, 0, s>>>(a);
+  else if (upt == 2) rope_kernel<T, D, 2><<<grid, threads, 0, s>>>(a);
+  else if (upt == 3) rope_kernel<T, D, 3><<<grid, threads, 0, s>>>(a);
+  else rope_kernel<T, D, 4><<<grid, threads, 0, s>>>(a);
+  return cudaGetLastError();
 }
 
 }  // namespace
@@ -124,28 +275,20 @@ cudaError_t launch_rope(bool bf16, const da_rope_plan& plan, int B, int H, int N
   a.pos_batch = pos_batch;
   a.H = H;
   a.N = N;
-  a.rows = (long long)B * N;
   a.xb = xs.batch; a.xh = xs.head; a.xn = xs.token;
   a.ob = os.batch; a.oh = os.head; a.on = os.token;
   for (int u = 0; u < 3; ++u) a.grid[u] = plan.grid[u];
-  a.full = weight && weight_width == H * d && H > 1;
+  a.norm = !weight ? kNoNorm : weight_width == d ? kHeadNorm : kFullNorm;
   a.eps = eps;
+  a.halves = plan.pairing == DA_ROPE_HALVES;
   int p = 0;
   for (int u = 0; u < 3; ++u)
     for (int j = 0; j < plan.axis_dims[u] / 2; ++j, ++p) {
       a.freq[p] = pow(plan.theta, -2.0 * j / plan.axis_dims[u]) / M_PI;
       a.axis[p] = (unsigned char)u;
     }
-  const int halves = plan.pairing == DA_ROPE_HALVES;
-  const unsigned grid = (unsigned)a.rows;
-  if (bf16) {
-    if (d == 128) rope_kernel<__nv_bfloat16, 128><<<grid, 128, 0, s>>>(a, halves);
-    else rope_kernel<__nv_bfloat16, 64><<<grid, 128, 0, s>>>(a, halves);
-  } else {
-    if (d == 128) rope_kernel<float, 128><<<grid, 128, 0, s>>>(a, halves);
-    else rope_kernel<float, 64><<<grid, 128, 0, s>>>(a, halves);
-  }
-  return cudaGetLastError();
+  if (bf16) return d == 128 ? launch_typed<__nv_bfloat16, 128>(a, B, s) : launch_typed<__nv_bfloat16, 64>(a, B, s);
+  return d == 128 ? launch_typed<float, 128>(a, B, s) : launch_typed<float, 64>(a, B, s);
 }
 
 }  // namespace da

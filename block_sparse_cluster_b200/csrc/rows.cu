@@ -26,6 +26,22 @@ enum { kNorm = 0, kNormI8 = 1, kQuantI8 = 2 };
 
 constexpr int kMaxWarps = 32;
 
+// The low bytes of four words as one word.
+__device__ __forceinline__ uint32_t low_bytes(const uint32_t* q) {
+  return __byte_perm(__byte_perm(q[0], q[1], 0x0040), __byte_perm(q[2], q[3], 0x0040), 0x5410);
+}
+
+// The larger of a and |b|; a NaN wins over every number.
+__device__ __forceinline__ float max_abs(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(fabsf(b)));
+  return r;
+}
+
+// 1.5 * 2^23: adding it to |u| <= 2^22 rounds u to the nearest integer, ties to even, and leaves that integer in the sum's
+// low bits, from where a code is taken as a byte without a conversion.
+constexpr float kRound = 12582912.f;
+
 template <int V>
 struct Pack;   // V consecutive elements as one aligned load
 template <>
@@ -34,7 +50,7 @@ struct Pack<1> {
   static __device__ __forceinline__ void load(const __nv_bfloat16* p, float* o) { o[0] = __bfloat162float(*p); }
   static __device__ __forceinline__ void store(float* p, const float* v) { *p = v[0]; }
   static __device__ __forceinline__ void store(__nv_bfloat16* p, const float* v) { *p = __float2bfloat16_rn(v[0]); }
-  static __device__ __forceinline__ void store_codes(int8_t* p, const int* q) { *p = (int8_t)q[0]; }
+  static __device__ __forceinline__ void store_codes(int8_t* p, const uint32_t* q) { *p = (int8_t)q[0]; }
 };
 template <>
 struct Pack<4> {
@@ -45,8 +61,8 @@ struct Pack<4> {
   static __device__ __forceinline__ void store(float* p, const float* v) {
     *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
   }
-  static __device__ __forceinline__ void store_codes(int8_t* p, const int* q) {
-    *reinterpret_cast<uint32_t*>(p) = (q[0] & 255) | (q[1] & 255) << 8 | (q[2] & 255) << 16 | (uint32_t)q[3] << 24;
+  static __device__ __forceinline__ void store_codes(int8_t* p, const uint32_t* q) {
+    *reinterpret_cast<uint32_t*>(p) = low_bytes(q);
   }
 };
 template <>
@@ -64,11 +80,8 @@ struct Pack<8> {
     *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
                                               pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
   }
-  static __device__ __forceinline__ void store_codes(int8_t* p, const int* q) {
-    uint2 o;
-    o.x = (q[0] & 255) | (q[1] & 255) << 8 | (q[2] & 255) << 16 | (uint32_t)q[3] << 24;
-    o.y = (q[4] & 255) | (q[5] & 255) << 8 | (q[6] & 255) << 16 | (uint32_t)q[7] << 24;
-    *reinterpret_cast<uint2*>(p) = o;
+  static __device__ __forceinline__ void store_codes(int8_t* p, const uint32_t* q) {
+    *reinterpret_cast<uint2*>(p) = make_uint2(low_bytes(q), low_bytes(q + 4));
   }
 };
 
@@ -82,14 +95,15 @@ struct RowArgs {
   float* scale;           // codes only
   long long rows;
   int width, head_dim;
-  int tokens;             // rows of one batch entry
+  int head_shift;         // log2 head_dim, or -1
+  int tokens;             // rows of one batch entry (blockIdx.y)
   long long x_batch, x_head, x_token, r_stride, sum_stride, out_stride;
   float eps;
 };
 
-// A group of kWarps * 32 threads owns a row (kWarps = 0: the whole block; one warp otherwise).
+// A warp (WARP_ROW) or the whole block owns a row.
 template <typename T, int V, int VPT, int MODE, bool WARP_ROW>
-__global__ void __launch_bounds__(WARP_ROW ? 128 : 1024)
+__global__ void __launch_bounds__(WARP_ROW ? 128 : 512)
 row_kernel(const RowArgs a) {
   __shared__ float s_sum[kMaxWarps];
   __shared__ uint32_t s_max[kMaxWarps];
@@ -97,13 +111,16 @@ row_kernel(const RowArgs a) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int gt = WARP_ROW ? lane : threadIdx.x;
   const int gsize = WARP_ROW ? 32 : blockDim.x;
-  const long long row = WARP_ROW ? (long long)blockIdx.x * (blockDim.x >> 5) + warp : blockIdx.x;
-  if (WARP_ROW && row >= a.rows) return;
-  const T* x = static_cast<const T*>(a.x) + (row / a.tokens) * a.x_batch + (row % a.tokens) * a.x_token;
+  const int token = WARP_ROW ? blockIdx.x * (blockDim.x >> 5) + warp : blockIdx.x;
+  if (WARP_ROW && token >= a.tokens) return;
+  const long long row = (long long)blockIdx.y * a.tokens + token;
+  const T* x = static_cast<const T*>(a.x) + blockIdx.y * a.x_batch + token * a.x_token;
   const T* r = MODE != kQuantI8 && a.residual ? static_cast<const T*>(a.residual) + row * a.r_stride : nullptr;
   const T* w = MODE != kQuantI8 ? static_cast<const T*>(a.weight) : nullptr;
   auto x_at = [&](int c) -> const T* {
-    return MODE == kQuantI8 ? x + (c / a.head_dim) * a.x_head + c % a.head_dim : x + c;
+    if (MODE != kQuantI8) return x + c;
+    const int h = a.head_shift >= 0 ? c >> a.head_shift : c / a.head_dim;
+    return x + h * a.x_head + (c - h * a.head_dim);
   };
 
   float v[VPT][V];
@@ -126,9 +143,9 @@ row_kernel(const RowArgs a) {
     for (int e = 0; e < V; ++e) ss = fmaf(v[i][e], v[i][e], ss);
   }
 
-  // t = v w, in place of the weight for the codes; |t|'s bits order as integers, NaN above all
+  // t = v w; its sum of squares is v's
   float t[MODE == kNorm ? 1 : VPT][V];
-  uint32_t top = 0;
+  float mine = 0.f;
   if (MODE != kNorm) {
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
@@ -139,11 +156,12 @@ row_kernel(const RowArgs a) {
       if (w && c < a.width) Pack<V>::load(w + c, wv);
 #pragma unroll
       for (int e = 0; e < V; ++e) {
-        t[i][e] = v[i][e] * wv[e];
-        top = max(top, __float_as_uint(fabsf(t[i][e])));
+        t[i][e] = MODE == kNormI8 ? v[i][e] * wv[e] : v[i][e];
+        mine = max_abs(mine, t[i][e]);
       }
     }
   }
+  uint32_t top = __float_as_uint(mine);   // not negative: orders as an integer, a NaN above all
 
   // sums and maxima over the group, in a fixed order
   if (MODE != kQuantI8) {
@@ -204,7 +222,7 @@ row_kernel(const RowArgs a) {
   if (MODE == kNormI8) {
     unsigned long long best = 0;
     const float close = m * (1.f - 4.76837158e-7f);   // 1 - 2^-21
-    if (m < INFINITY) {
+    if (mine >= close) {   // few threads; none where m is not finite, but infinity, whose row is answered below
 #pragma unroll
       for (int i = 0; i < VPT; ++i) {
 #pragma unroll
@@ -230,20 +248,29 @@ row_kernel(const RowArgs a) {
   if (gt == 0) a.scale[row] = finite ? m * (1.f / 127.f) * (m > 0.f ? rms : 1.f) : __uint_as_float(0x7fffffffu);
   // below 1e-30 the fp32 quotient may lose more than its error bound (subnormal t, 127 / m infinite)
   const bool tiny = m < 1e-30f;
-  const float inv = 127.f / m;
+  const float inv = finite ? 127.f / m : 0.f;
   int8_t* q = static_cast<int8_t*>(a.out) + row * a.out_stride;
   T* sum = MODE == kNormI8 && a.sum_out ? static_cast<T*>(a.sum_out) + row * a.sum_stride : nullptr;
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
     const int c = (i * gsize + gt) * V;
     if (c < a.width) {
-      int code[V];
+      uint32_t code[V];
+      float far = 0.f;   // the largest distance of a quotient from its code
 #pragma unroll
       for (int e = 0; e < V; ++e) {
-        const float u = t[i][e] * inv, n = rintf(u);
-        code[e] = (int)n;
-        if (tiny || fabsf(u - n) > 0.5f - 6.1035156e-5f) code[e] = m > 0.f ? (int)rint(exact_t(c + e) * 127.0 / m64) : 0;
-        if (!finite) code[e] = 0;
+        const float u = t[i][e] * inv, k = u + kRound;
+        code[e] = __float_as_uint(k);
+        far = fmaxf(far, fabsf(u - (k - kRound)));
+      }
+      if (tiny || far > 0.5f - 6.1035156e-5f) {
+#pragma unroll
+        for (int e = 0; e < V; ++e)
+          code[e] = m > 0.f ? (uint32_t)(int)rint(exact_t(c + e) * 127.0 / m64) : 0u;
+      }
+      if (!finite) {
+#pragma unroll
+        for (int e = 0; e < V; ++e) code[e] = 0u;
       }
       Pack<V>::store_codes(q + c, code);
       // the sum last: its buffer may be an input's, which the fp64 codes read again
@@ -252,21 +279,25 @@ row_kernel(const RowArgs a) {
   }
 }
 
+// A row of up to 128 vectors is a warp's, so that it needs no barrier; longer ones take the block that holds them
+// with VPT vectors a thread in at most 512 threads.
 template <typename T, int V, int MODE>
 cudaError_t launch_rows_v(const RowArgs& a, cudaStream_t s) {
   const int nvec = (a.width + V - 1) / V;
+  const unsigned batch = (unsigned)(a.rows / a.tokens);
   if (nvec <= 128) {
-    const unsigned grid = (unsigned)((a.rows + 3) / 4);
+    const dim3 grid((unsigned)((a.tokens + 3) / 4), batch);
     if (nvec <= 32) row_kernel<T, V, 1, MODE, true><<<grid, 128, 0, s>>>(a);
     else if (nvec <= 64) row_kernel<T, V, 2, MODE, true><<<grid, 128, 0, s>>>(a);
     else row_kernel<T, V, 4, MODE, true><<<grid, 128, 0, s>>>(a);
     return cudaGetLastError();
   }
-  const unsigned grid = (unsigned)a.rows;
+  const dim3 grid((unsigned)a.tokens, batch);
   auto threads = [&](int vpt) { return ((nvec + vpt - 1) / vpt + 31) / 32 * 32; };
-  if (nvec <= 2048) row_kernel<T, V, 2, MODE, false><<<grid, threads(2), 0, s>>>(a);
-  else if (V < 8 && nvec <= 4096) row_kernel<T, V, 4, MODE, false><<<grid, threads(4), 0, s>>>(a);
-  else if (V < 4) row_kernel<T, V, V < 4 ? 16 : 4, MODE, false><<<grid, threads(16), 0, s>>>(a);
+  if (nvec <= 1024) row_kernel<T, V, 2, MODE, false><<<grid, threads(2), 0, s>>>(a);
+  else if (nvec <= 2048) row_kernel<T, V, 4, MODE, false><<<grid, threads(4), 0, s>>>(a);
+  else if (V < 8 && nvec <= 4096) row_kernel<T, V, V < 8 ? 8 : 4, MODE, false><<<grid, threads(8), 0, s>>>(a);
+  else if (V < 4) row_kernel<T, V, V < 4 ? 32 : 4, MODE, false><<<grid, threads(32), 0, s>>>(a);
   else return cudaErrorInvalidValue;
   return cudaGetLastError();
 }
@@ -295,14 +326,16 @@ cudaError_t launch_rows(bool bf16, const RowArgs& a, cudaStream_t s) {
 cudaError_t launch_rms_norm(bool bf16, long long rows, int width, const void* x, long long x_stride,
                             const void* residual, long long r_stride, const void* weight, float eps, void* sum_out,
                             long long sum_stride, void* out, long long out_stride, float* scale, cudaStream_t s) {
-  const RowArgs a{x, residual, weight, sum_out, out, scale, rows, width, width, (int)rows,
+  const RowArgs a{x, residual, weight, sum_out, out, scale, rows, width, width, -1, (int)rows,
                   0, 0, x_stride, r_stride, sum_stride, out_stride, eps};
   return scale ? launch_rows<kNormI8>(bf16, a, s) : launch_rows<kNorm>(bf16, a, s);
 }
 
 cudaError_t launch_quantize_i8(bool bf16, int B, int H, int N, int d, const void* x, const da_head_strides& xs,
                                int8_t* q, long long q_stride, float* scale, cudaStream_t s) {
-  const RowArgs a{x, nullptr, nullptr, nullptr, q, scale, (long long)B * N, H * d, d, N,
+  int shift = 0;
+  while ((1 << shift) < d) ++shift;
+  const RowArgs a{x, nullptr, nullptr, nullptr, q, scale, (long long)B * N, H * d, d, (1 << shift) == d ? shift : -1, N,
                   xs.batch, xs.head, xs.token, 0, 0, q_stride, 0.f};
   return launch_rows<kQuantI8>(bf16, a, s);
 }

@@ -349,7 +349,7 @@ DA_API da_status da_rms_norm_i8(int64_t rows, int width, da_dtype dtype, const v
  * with m = max |x| over the row, q = nearest integer to 127 x / m (ties to even), scale = m / 127.
  * x: [B,H,N,d] of dtype with the given strides (the attention's O; a matrix of weights is B = H = 1,
  * one row per output channel).  q: [B*N, H*d] int8, scale: [B*N] fp32; rows of zeros and rows
- * with infinities or NaN as in da_rms_norm_i8.  H * d <= 16384.
+ * with infinities or NaN as in da_rms_norm_i8.  H * d <= 16384 (DA_ERR_UNSUPPORTED above), B <= 65535.
  */
 DA_API da_status da_quantize_i8(int B, int H, int N, int d, da_dtype dtype, const void* x,
                                 const da_head_strides* x_strides, int8_t* q, int64_t q_stride, float* scale,
@@ -393,7 +393,7 @@ typedef struct {
  * the pairs given to the axes in order (the first axis_dims[0] / 2 to time, ...), becomes
  * (a cos f - b sin f, a sin f + b cos f), f = position on its axis times the pair's frequency.
  * x, out: [B,H,N,d] of dtype with their strides (x may be a slice of a projection's token rows,
- * out the attention's [B,H,N,d]); bases, strides and weight on 16 bytes.  d is 64 or 128.
+ * out the attention's [B,H,N,d]); bases, strides and weight on 16 bytes.  d is 64 or 128; B and H <= 65535.
  * positions: [N,3] int32 (time, height, width; any int32, negative ones turn back), one list for each
  * batch entry positions_batch elements apart (0: one list for all), or NULL: the plan's grid.  Tokens behind
  * the grid (text behind a video) are not turned: they are copied, or normed only.

@@ -8,21 +8,24 @@
 //   quantize:  t = x,  scale = m / 127
 // A row of zeros has scale 0 and codes 0; a row with an infinity or a NaN has scale NaN and codes 0.
 //
-// Codes are the nearest ones of the exact quotient.  fp32 gives t * (127 / m) to within kNear of it; only where
-// that lies so close to a border k + 1/2 is the side decided by comparing 127 |t| with (k + 1/2) m in fp64,
-// from the inputs.  The row's maximum is likewise found in fp32 and, where such an element turns up, taken in
-// fp64 over the few elements within 2^-21 of it.
+// Codes are the nearest ones of the exact quotient.  fp32 gives t * (127 / m) to within kNear of it; where that lies
+// so close to a border k + 1/2, the codes of the vector are taken again from the inputs, comparing 127 |t| with
+// (k + 1/2) m in fp64.  The row's maximum is likewise found in fp32 and, where such a vector turns up, taken in fp64
+// over the few elements within 2^-21 of it.
 //
 // A warp or a block owns a row and keeps it in registers between the reduction and the output, so every
-// input is read once and every output written once.  The bound is HBM, but instructions are close behind (a bf16 row
-// of codes gives an SM 24 of them for each 32 elements at HBM's rate): arithmetic is done on packed pairs,
-// codes are rounded by one addition, and a thread holds many elements so that a row's fixed work is spread.
+// input is read once and every output written once.  The bound is HBM, but instructions are close behind (for bf16
+// codes an SM has about 40 of them for each 32 elements at HBM's rate): arithmetic is done on packed pairs, codes are
+// rounded by one addition, and a thread holds many elements so that a row's fixed work is spread.  Walking the rows
+// with as many blocks as the GPU holds, each row's loads ahead of the row in front, was slower (75600 x 5120 codes:
+// 338 us against 264; norm: 481 against 451): the registers of the loads ahead cost more warps than they hide.
 #include "da_common.cuh"
 #include "da_internal.h"
 
 namespace da {
 
 namespace {
+
 
 enum { kNorm = 0, kNormI8 = 1, kQuantI8 = 2 };
 
@@ -31,6 +34,13 @@ constexpr int kMaxWarps = 16;
 // 1.5 * 2^23: adding it to |u| <= 2^22 rounds u to the nearest integer, ties to even, and leaves that integer in the sum's
 // low bits, from where a code is taken as a byte without a conversion.
 constexpr float kRound = 12582912.f;
+
+// bf16 rows without a norm: t = T 2^a and m = M 2^b with 8-bit integers T and M, so 127 t / m is a border k + 1/2 or
+// misses it by a 254 * 255th of itself: |254 T - (2k + 1) M 2^(b - a)| is a whole number.  fp32's u = t * (127 / m), off by
+// 2^-24, is first rounded to 18 bits, as h = p - (p - u) with p = 65 u: that moves it by at most 2^-18 of itself, onto the
+// border in the one case (a border has 8 bits) and not as far as the border in the other.  Rounding h to an integer
+// then sends ties to even, and no element needs a second look.
+constexpr float kSplit = 65.f;
 
 // How far t * (127 / m) may be from the exact quotient, with u = 2^-24: the quantiser's t and m are exact and 127 / m
 // rounds once, 127 u < 2^-16; the norm's t rounds twice (sum, product) and so does the m taken from it: 5 * 127 u < 2^-14.
@@ -42,10 +52,14 @@ __device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
-// The largest of a, |b| and |c|; a NaN wins over every number.
-__device__ __forceinline__ float max_abs(float a, float b, float c) {
+__device__ __forceinline__ float max3_nan(float a, float b, float c) {   // a NaN wins over every number
   float r;
-  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(fabsf(b)), "f"(fabsf(c)));
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+__device__ __forceinline__ float fmin3(float a, float b, float c) {
+  float r;
+  asm("min.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
 // The low bytes of four words as one word.
@@ -83,8 +97,8 @@ struct Pack<float, 4> {
     *reinterpret_cast<uint32_t*>(p) = low_bytes(q[0], q[1], q[2], q[3]);
   }
   static __device__ __forceinline__ uint32_t max_bits(uint32_t m, const Raw& r) {
-    m = max(max(m, __float_as_uint(fabsf(r.x))), __float_as_uint(fabsf(r.y)));
-    return max(max(m, __float_as_uint(fabsf(r.z))), __float_as_uint(fabsf(r.w)));
+    m = __vimax3_u32(m, __float_as_uint(fabsf(r.x)), __float_as_uint(fabsf(r.y)));
+    return __vimax3_u32(m, __float_as_uint(fabsf(r.z)), __float_as_uint(fabsf(r.w)));
   }
   static __device__ __forceinline__ uint32_t max_float(uint32_t m) { return m; }
 };
@@ -110,8 +124,8 @@ struct Pack<__nv_bfloat16, 8> {
   }
   // two maxima side by side, in the halves of a word
   static __device__ __forceinline__ uint32_t max_bits(uint32_t m, const Raw& r) {
-    m = __vmaxu2(__vmaxu2(m, r.x & 0x7fff7fffu), r.y & 0x7fff7fffu);
-    return __vmaxu2(__vmaxu2(m, r.z & 0x7fff7fffu), r.w & 0x7fff7fffu);
+    m = __vimax3_u16x2(m, r.x & 0x7fff7fffu, r.y & 0x7fff7fffu);
+    return __vimax3_u16x2(m, r.z & 0x7fff7fffu, r.w & 0x7fff7fffu);
   }
   static __device__ __forceinline__ uint32_t max_float(uint32_t m) { return max(m << 16, m & 0xffff0000u); }
 };
@@ -126,19 +140,48 @@ struct RowArgs {
   float* scale;           // codes only
   long long rows;
   int width, head_dim;
-  int head_shift;         // log2 head_dim (30 with one head), or -1
   int tokens;             // rows of one batch entry (blockIdx.y)
   long long x_batch, x_head, x_token, r_stride, sum_stride, out_stride;
-  float eps;
+  float eps, inv_width;
+  long long x_step;       // from a thread's vector of x to its next one, or -1 where that is not the same for all
 };
+
+// Element c of a row of x.
+__device__ __forceinline__ long long x_offset(const RowArgs& a, int c) {
+  const int h = c / a.head_dim;
+  return h * a.x_head + (c - h * a.head_dim);
+}
+
+// t = (x + r) w in fp64 of the V elements from column c on.
+template <typename T, int V>
+__device__ __forceinline__ void exact_t(const RowArgs& a, const T* x, const T* r, const T* w, int c, double* t) {
+  using P = Pack<T, V>;
+  float f[V];
+  P::unpack(P::load(x + x_offset(a, c)), f);
+#pragma unroll
+  for (int e = 0; e < V; ++e) t[e] = f[e];
+  if (r) {
+    P::unpack(P::load(r + c), f);
+#pragma unroll
+    for (int e = 0; e < V; ++e) t[e] += f[e];
+  }
+  if (w) {
+    P::unpack(P::load(w + c), f);
+#pragma unroll
+    for (int e = 0; e < V; ++e) t[e] *= f[e];
+  }
+}
 
 // A warp (WARP_ROW) or the whole block owns a row; each of its threads holds VPT vectors of V elements.
 template <typename T, int V, int VPT, int MODE, bool WARP_ROW>
 __global__ void __launch_bounds__(WARP_ROW ? 128 : 512)
 row_kernel(const RowArgs a) {
   using P = Pack<T, V>;
-  constexpr int E = VPT * V;   // elements of a thread, an even number
-  static_assert(E % 2 == 0, "elements are worked on in pairs");
+  constexpr int E = VPT * V;                  // elements of a thread
+  constexpr int kChunk = V < 2 ? 2 : V;       // elements that are worked on together: a vector, or a pair of single ones
+  static_assert(E % kChunk == 0 && VPT <= 32, "elements are worked on in pairs, and vectors noted in 32 bits");
+  constexpr bool kCodes = MODE != kNorm, kScaled = MODE != kQuantI8;   // codes come out; the norm's factor is formed
+  constexpr bool kSnaps = !kScaled && sizeof(T) == 2;
   __shared__ float s_sum[kMaxWarps];
   __shared__ uint32_t s_max[kMaxWarps];
   __shared__ unsigned long long s_top;
@@ -149,24 +192,29 @@ row_kernel(const RowArgs a) {
   if (WARP_ROW && token >= a.tokens) return;
   const long long row = (long long)blockIdx.y * a.tokens + token;
   const T* x = static_cast<const T*>(a.x) + blockIdx.y * a.x_batch + token * a.x_token;
-  const T* r = MODE != kQuantI8 && a.residual ? static_cast<const T*>(a.residual) + row * a.r_stride : nullptr;
-  const T* w = MODE != kQuantI8 ? static_cast<const T*>(a.weight) : nullptr;
-  auto x_at = [&](int c) -> const T* {
-    if (MODE != kQuantI8) return x + c;
-    const int h = a.head_shift >= 0 ? c >> a.head_shift : c / a.head_dim;
-    return x + h * a.x_head + (c - h * a.head_dim);
-  };
+  const T* r = kScaled && a.residual ? static_cast<const T*>(a.residual) + row * a.r_stride : nullptr;
+  const T* w = kScaled ? static_cast<const T*>(a.weight) : nullptr;
   auto column = [&](int i) { return (i * gsize + gt) * V; };
+  auto inside = [&](int i) { return min(column(i), a.width - V); };   // a vector of the row for every thread
 
   // the row: the quantiser keeps it as it was loaded, the norms as fp32 sums in pairs
-  typename P::Raw raw[VPT], res[MODE == kQuantI8 ? 1 : VPT];
-  uint64_t v[MODE == kQuantI8 ? 1 : E / 2];
+  typename P::Raw raw[VPT], res[kScaled ? VPT : 1];
+  uint64_t v[kScaled ? E / 2 : 1];
+  if (kScaled) {
 #pragma unroll
-  for (int i = 0; i < VPT; ++i) {
-    raw[i] = P::zero();
-    if (column(i) < a.width) raw[i] = P::load(x_at(column(i)));
+    for (int i = 0; i < VPT; ++i) {
+      raw[i] = P::zero();
+      if (column(i) < a.width) raw[i] = P::load(x + column(i));
+    }
+  } else if (a.x_step >= 0) {   // threads beyond the row repeat vectors of it, which change no maximum
+    const T* x0 = x + x_offset(a, inside(0));
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) raw[i] = P::load(column(i) < a.width ? x0 + i * a.x_step : x);
+  } else {
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) raw[i] = P::load(x + x_offset(a, inside(i)));
   }
-  if (MODE != kQuantI8) {
+  if (kScaled) {
     if (r) {
 #pragma unroll
       for (int i = 0; i < VPT; ++i) {
@@ -186,29 +234,48 @@ row_kernel(const RowArgs a) {
       for (int p = 0; p < E / 2; ++p) v[p] = f2_add(v[p], f2_pack(f[2 * p], f[2 * p + 1]));
     }
   }
-  // pairs of t = v w of the vectors that hold element pair p; weights come from L1 both times they are needed
-  auto times_weight = [&](uint64_t (&t)[E / 2]) {
-    if (MODE == kQuantI8) {
-      float f[E];
+  // t = v w of chunk k in pairs; weights come from L1 each time, so that they take no registers
+  auto chunk_t = [&](bool weighted, int k, uint64_t (&t)[kChunk / 2]) {
+    if (!kScaled || weighted) {
+      float f[kChunk];
 #pragma unroll
-      for (int i = 0; i < VPT; ++i) P::unpack(raw[i], f + i * V);
+      for (int e = 0; e < kChunk; e += V) {
+        const int i = (k * kChunk + e) / V;
+        P::unpack(kScaled ? P::load(w + inside(i)) : raw[i], f + e);
+      }
 #pragma unroll
-      for (int p = 0; p < E / 2; ++p) t[p] = f2_pack(f[2 * p], f[2 * p + 1]);
-    } else if (w) {
-      float f[E];
+      for (int e = 0; e < kChunk; e += 2) t[e / 2] = f2_pack(f[e], f[e + 1]);
+    }
+    if (kScaled) {
 #pragma unroll
-      for (int i = 0; i < VPT; ++i) P::unpack(column(i) < a.width ? P::load(w + column(i)) : P::zero(), f + i * V);
+      for (int e = 0; e < kChunk; e += 2) {
+        const uint64_t ve = v[(k * kChunk + e) / 2];
+        t[e / 2] = weighted ? f2_mul(ve, t[e / 2]) : ve;
+      }
+    }
+  };
+  // f(k, t) for every chunk; whether there is a weight is decided once, outside the loop
+  auto for_chunks = [&](auto f) {
+    if (kScaled && w) {
 #pragma unroll
-      for (int p = 0; p < E / 2; ++p) t[p] = f2_mul(v[p], f2_pack(f[2 * p], f[2 * p + 1]));
+      for (int k = 0; k < E / kChunk; ++k) {
+        uint64_t t[kChunk / 2];
+        chunk_t(true, k, t);
+        f(k, t);
+      }
     } else {
 #pragma unroll
-      for (int p = 0; p < E / 2; ++p) t[p] = v[p];
+      for (int k = 0; k < E / kChunk; ++k) {
+        uint64_t t[kChunk / 2];
+        chunk_t(false, k, t);
+        f(k, t);
+      }
     }
   };
 
   float ss = 0.f;
   uint32_t mine = 0;   // bits of the thread's max |t|: not negative, so it orders as an integer, a NaN above all
-  if (MODE != kQuantI8) {
+  if (kScaled) {
     uint64_t s2 = 0;
 #pragma unroll
     for (int p = 0; p < E / 2; ++p) s2 = f2_fma(v[p], v[p], s2);
@@ -221,140 +288,149 @@ row_kernel(const RowArgs a) {
     for (int i = 0; i < VPT; ++i) mine = P::max_bits(mine, raw[i]);
     mine = P::max_float(mine);
   } else if (MODE == kNormI8) {
-    uint64_t t[E / 2];
-    times_weight(t);
-    float top = 0.f;
+    float high = 0.f, low = 0.f;
+    for_chunks([&](int, uint64_t (&t)[kChunk / 2]) {
 #pragma unroll
-    for (int p = 0; p < E / 2; ++p) {
-      float lo, hi;
-      f2_unpack(t[p], lo, hi);
-      top = max_abs(top, lo, hi);
-    }
-    mine = __float_as_uint(top);
+      for (int e = 0; e < kChunk; e += 2) {
+        float lo, hi;
+        f2_unpack(t[e / 2], lo, hi);
+        high = max3_nan(high, lo, hi);
+        low = fmin3(low, lo, hi);
+      }
+    });
+    mine = max(__float_as_uint(fabsf(high)), __float_as_uint(fabsf(low)));
   }
 
   // sums and maxima over the row's threads, in a fixed order
   uint32_t top = mine;
-  if (MODE != kQuantI8) {
+  if (kScaled) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
   }
-  if (MODE != kNorm) top = __reduce_max_sync(0xffffffffu, top);
+  if (kCodes) top = __reduce_max_sync(0xffffffffu, top);
   if (!WARP_ROW) {
     if (lane == 0) {
       s_sum[warp] = ss;
       s_max[warp] = top;
     }
-    if (threadIdx.x == 0) s_top = 0;
+    if (MODE == kNormI8 && threadIdx.x == 0) s_top = 0;
     __syncthreads();
     const int nw = blockDim.x >> 5;
-    if (MODE != kQuantI8) {
+    if (kScaled) {
       ss = lane < nw ? s_sum[lane] : 0.f;
 #pragma unroll
       for (int o = 8; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
       ss = __shfl_sync(0xffffffffu, ss, 0);
     }
-    if (MODE != kNorm) top = __reduce_max_sync(0xffffffffu, lane < nw ? s_max[lane] : 0u);
+    if (kCodes) top = __reduce_max_sync(0xffffffffu, lane < nw ? s_max[lane] : 0u);
   }
-  const float rms = MODE == kQuantI8 ? 1.f : rsqrtf(ss / (float)a.width + a.eps);
-  T* sum = MODE != kQuantI8 && a.sum_out ? static_cast<T*>(a.sum_out) + row * a.sum_stride : nullptr;
+  const float rms = kScaled ? rsqrtf(ss * a.inv_width + a.eps) : 1.f;
+
+  T* sum = kScaled && a.sum_out ? static_cast<T*>(a.sum_out) + row * a.sum_stride : nullptr;
+  auto store_chunk = [&](T* p, int k, const uint64_t* t) {
+    float f[kChunk];
+#pragma unroll
+    for (int e = 0; e < kChunk; e += 2) f2_unpack(t[e / 2], f[e], f[e + 1]);
+#pragma unroll
+    for (int e = 0; e < kChunk; e += V) {
+      const int c = column((k * kChunk + e) / V);
+      if (c < a.width) P::store(p + c, f + e);
+    }
+  };
   auto store_sum = [&]() {
+    if (kScaled && sum) {
 #pragma unroll
-    for (int i = 0; i < VPT; ++i)
-      if (column(i) < a.width) {
-        float f[V < 2 ? 2 : V];
-#pragma unroll
-        for (int e = 0; e < V; e += 2) f2_unpack(v[(i * V + e) / 2], f[e], f[e + 1]);
-        P::store(sum + column(i), V == 1 ? f + (i & 1) : f);
-      }
+      for (int k = 0; k < E / kChunk; ++k) store_chunk(sum, k, v + k * kChunk / 2);
+    }
   };
 
   if (MODE == kNorm) {
     T* out = static_cast<T*>(a.out) + row * a.out_stride;
-    if (sum) store_sum();
-    uint64_t t[E / 2];
-    times_weight(t);
+    store_sum();
     const uint64_t rms2 = f2_pack(rms, rms);
+    for_chunks([&](int k, uint64_t (&t)[kChunk / 2]) {
 #pragma unroll
-    for (int p = 0; p < E / 2; ++p) t[p] = f2_mul(t[p], rms2);
-#pragma unroll
-    for (int i = 0; i < VPT; ++i)
-      if (column(i) < a.width) {
-        float f[V < 2 ? 2 : V];
-#pragma unroll
-        for (int e = 0; e < V; e += 2) f2_unpack(t[(i * V + e) / 2], f[e], f[e + 1]);
-        P::store(out + column(i), V == 1 ? f + (i & 1) : f);
-      }
+      for (int p = 0; p < kChunk / 2; ++p) t[p] = f2_mul(t[p], rms2);
+      store_chunk(out, k, t);
+    });
     return;
   }
 
   const float m = __uint_as_float(top);
-  const bool finite = m < INFINITY;
-  if (gt == 0) a.scale[row] = finite ? m * (1.f / 127.f) * (m > 0.f ? rms : 1.f) : __uint_as_float(0x7fffffffu);
+  int8_t* q = static_cast<int8_t*>(a.out) + row * a.out_stride;
+  if (!(m < INFINITY)) {   // an infinity or a NaN: the same for the whole row
+    if (gt == 0) a.scale[row] = __uint_as_float(0x7fffffffu);
+    const uint32_t none[kChunk] = {};
+#pragma unroll
+    for (int i = 0; i < VPT; ++i)
+      if (column(i) < a.width) P::store_codes(q + column(i), none);
+    store_sum();
+    return;
+  }
+  if (gt == 0) a.scale[row] = m * (1.f / 127.f) * (m > 0.f ? rms : 1.f);
   // below 1e-30 fp32 may lose more than kNear (subnormal t, 127 / m infinite): every code in fp64, by division
   const bool tiny = m > 0.f && m < 1e-30f;
-  const float inv = finite && m >= 1e-30f ? 127.f / m : 0.f;
-  int8_t* q = static_cast<int8_t*>(a.out) + row * a.out_stride;
+  const float inv = m >= 1e-30f ? 127.f / m : 0.f;
   uint32_t open = 0;   // vectors of this thread with an element next to a border, or all of them
-  uint64_t t[E / 2];
-  times_weight(t);
-  {
-    const uint64_t inv2 = f2_pack(inv, inv), round2 = f2_pack(kRound, kRound), minus2 = f2_pack(-1.f, -1.f);
+  const uint64_t inv2 = f2_pack(inv, inv), round2 = f2_pack(kRound, kRound), minus2 = f2_pack(-1.f, -1.f);
+  const uint64_t split2 = f2_pack(kSplit * inv, kSplit * inv), back2 = f2_pack(-inv, -inv);
+  for_chunks([&](int k, uint64_t (&t)[kChunk / 2]) {
+    uint32_t code[kChunk];
+    float far = 0.f;   // the largest distance of a quotient from its code
 #pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-      uint32_t code[V < 2 ? 2 : V];
-      float far = 0.f;   // the largest distance of a quotient from its code
-#pragma unroll
-      for (int e = 0; e < V; e += 2) {
-        const uint64_t te = t[(i * V + e) / 2];
-        const uint64_t k = f2_fma(te, inv2, round2);
-        const uint64_t d = f2_fma(te, inv2, f2_fma(k, minus2, round2));
-        float lo, hi;
-        f2_unpack(k, lo, hi);
-        code[e] = __float_as_uint(lo);
-        code[e + 1] = __float_as_uint(hi);
-        f2_unpack(d, lo, hi);
-        if (V == 1) far = fabsf((i & 1) ? hi : lo);
-        else far = fmax3(far, fabsf(lo), fabsf(hi));
+    for (int e = 0; e < kChunk; e += 2) {
+      uint64_t n;
+      if (kSnaps) {
+        const uint64_t p = f2_mul(t[e / 2], split2);
+        n = f2_add(f2_fma(f2_fma(t[e / 2], back2, p), minus2, p), round2);
+      } else {
+        n = f2_fma(t[e / 2], inv2, round2);
       }
-      if (!finite) {   // the same for the whole row; products of infinities and NaN are no codes
-#pragma unroll
-        for (int e = 0; e < (V < 2 ? 2 : V); ++e) code[e] = 0u;
-        far = 0.f;
-      }
-      if (column(i) < a.width) {
-        if (tiny || far > 0.5f - kNear<MODE>) open |= 1u << i;
-        P::store_codes(q + column(i), V == 1 ? code + (i & 1) : code);
+      float lo, hi;
+      f2_unpack(n, lo, hi);
+      code[e] = __float_as_uint(lo);
+      code[e + 1] = __float_as_uint(hi);
+      if (!kSnaps) {
+        f2_unpack(f2_fma(t[e / 2], inv2, f2_fma(n, minus2, round2)), lo, hi);
+        far = fmax3(far, fabsf(lo), fabsf(hi));
       }
     }
-  }
+    if (far > 0.5f - kNear<MODE>) open |= (kChunk > V ? 3u : 1u) << (k * kChunk / V);
+#pragma unroll
+    for (int e = 0; e < kChunk; e += V) {
+      const int c = column((k * kChunk + e) / V);
+      if (c < a.width) P::store_codes(q + c, code + e);
+    }
+  });
+  if (tiny) open = ~0u >> (32 - VPT);
 
-  // t of one element in fp64, from the inputs
-  auto exact_t = [&](int c) -> double {
-    double d = to_f32(*x_at(c));
-    if (r) d += to_f32(r[c]);
-    if (w) d *= to_f32(w[c]);
-    return d;
-  };
-  const bool any = MODE == kQuantI8 ? open != 0 : WARP_ROW ? __any_sync(0xffffffffu, open) : __syncthreads_or(open);
+  const bool any = !kScaled ? open != 0 : WARP_ROW ? __any_sync(0xffffffffu, open != 0) : __syncthreads_or(open != 0);
   if (any) {
     double m64 = m;
     if (MODE == kNormI8) {
       unsigned long long best = 0;
       const float close = tiny ? 0.f : m * (1.f - 4.76837158e-7f);   // 1 - 2^-21
-      uint64_t near = 0;   // elements
       if (__uint_as_float(mine) >= close) {
+        uint32_t near = 0;   // vectors with an element this close to the maximum
+        for_chunks([&](int k, uint64_t (&t)[kChunk / 2]) {
+          float high = 0.f;
 #pragma unroll
-        for (int p = 0; p < E / 2; ++p) {
-          float lo, hi;
-          f2_unpack(t[p], lo, hi);
-          if (fabsf(lo) >= close) near |= 1ull << (2 * p);
-          if (fabsf(hi) >= close) near |= 2ull << (2 * p);
+          for (int e = 0; e < kChunk; e += 2) {
+            float lo, hi;
+            f2_unpack(t[e / 2], lo, hi);
+            high = fmax3(high, fabsf(lo), fabsf(hi));
+          }
+          if (high >= close) near |= (kChunk > V ? 3u : 1u) << (k * kChunk / V);
+        });
+#pragma unroll 1
+        for (; near; near &= near - 1) {
+          const int c = column(__ffs((int)near) - 1);
+          if (c >= a.width) continue;
+          double t[V];
+          exact_t<T, V>(a, x, r, w, c, t);
+#pragma unroll
+          for (int e = 0; e < V; ++e) best = max(best, (unsigned long long)__double_as_longlong(fabs(t[e])));
         }
-      }
-      for (; near; near &= near - 1) {
-        const int e = __ffsll((long long)near) - 1, c = column(e / V) + e % V;
-        if (c < a.width) best = max(best, (unsigned long long)__double_as_longlong(fabs(exact_t(c))));
       }
       if (WARP_ROW) {
 #pragma unroll
@@ -366,44 +442,63 @@ row_kernel(const RowArgs a) {
       }
       m64 = __longlong_as_double((long long)best);
     }
-    uint64_t near = 0;
+#pragma unroll 1
+    for (; open; open &= open - 1) {
+      const int c = column(__ffs((int)open) - 1);
+      if (c >= a.width) continue;
+      uint32_t code[V];
+      if (tiny) {
+        double t[V];
+        exact_t<T, V>(a, x, r, w, c, t);
 #pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-      if (open >> i & 1) {
+        for (int e = 0; e < V; ++e) code[e] = (uint32_t)(int)rint(127.0 * t[e] / m64);
+      } else if (MODE == kQuantI8) {
+        // t and m are exact, so fp32 tells the side: 254 |t| against (2k + 1) m, the product in two parts, both
+        // scaled down so that neither overflows
+        float f[V];
+        P::unpack(P::load(x + x_offset(a, c)), f);
 #pragma unroll
         for (int e = 0; e < V; ++e) {
-          float lo, hi;
-          f2_unpack(t[(i * V + e) / 2], lo, hi);
-          const float u = fabsf((i * V + e) & 1 ? hi : lo) * inv;
-          if (tiny || fabsf(u - floorf(u) - 0.5f) < 2.f * kNear<MODE>) near |= 1ull << (i * V + e);
+          const float size = fabsf(f[e]), k = truncf(size * inv), odd = fmaf(2.f, k, 1.f), ms = m * 0x1p-10f;
+          const float high = odd * ms, low = fmaf(odd, ms, -high), d = fmaf(254.f, size * 0x1p-10f, -high);
+          const int n = (int)k, up = d > low || (d == low && (n & 1));
+          code[e] = (uint32_t)(f[e] < 0.f ? -(n + up) : n + up);
+        }
+      } else {
+        double t[V];
+        exact_t<T, V>(a, x, r, w, c, t);
+#pragma unroll
+        for (int e = 0; e < V; ++e) {   // k or k + 1, by the side of the border between them; on it, the even one
+          const double size = 127.0 * fabs(t[e]);
+          const float k = truncf(fabsf((float)t[e]) * inv);
+          const double border = (double)(k + 0.5f) * m64;
+          const int n = (int)k, up = size > border || (size == border && (n & 1));
+          code[e] = (uint32_t)(t[e] < 0 ? -(n + up) : n + up);
         }
       }
-    }
-    for (; near; near &= near - 1) {
-      const int e = __ffsll((long long)near) - 1, c = column(e / V) + e % V;
-      const double d = exact_t(c), size = 127.0 * fabs(d);
-      double k;
-      if (tiny) {
-        k = rint(size / m64);
-      } else {
-        k = floorf(fabsf((float)d) * inv);   // below the border that t lies at
-        const double border = (k + 0.5) * m64;
-        if (size > border || (size == border && ((int)k & 1))) k += 1.0;
-      }
-      q[c] = (int8_t)(d < 0 ? -(int)k : (int)k);
+      P::store_codes(q + c, code);
     }
   }
   // the sum last: its buffer may be an input's, which the fp64 codes read again
-  if (MODE == kNormI8 && sum) store_sum();
+  store_sum();
+}
+
+// How far apart a thread's vectors of x lie, if its next one, `columns` further, is in the same place of a later head.
+long long vector_step(const RowArgs& a, int columns) {
+  if (a.head_dim == a.width) return columns;
+  return columns % a.head_dim == 0 ? columns / a.head_dim * a.x_head : -1;
 }
 
 template <typename T, int V, int VPT, int MODE>
-void launch_warp_rows(const RowArgs& a, unsigned batch, cudaStream_t s) {
+void launch_warp_rows(RowArgs a, unsigned batch, cudaStream_t s) {
+  a.x_step = vector_step(a, 32 * V);
   row_kernel<T, V, VPT, MODE, true><<<dim3((unsigned)((a.tokens + 3) / 4), batch), 128, 0, s>>>(a);
 }
 template <typename T, int V, int VPT, int MODE>
-void launch_block_rows(const RowArgs& a, unsigned batch, int nvec, cudaStream_t s) {
-  row_kernel<T, V, VPT, MODE, false><<<dim3((unsigned)a.tokens, batch), ((nvec + VPT - 1) / VPT + 31) / 32 * 32, 0, s>>>(a);
+void launch_block_rows(RowArgs a, unsigned batch, int nvec, cudaStream_t s) {
+  const int threads = ((nvec + VPT - 1) / VPT + 31) / 32 * 32;
+  a.x_step = vector_step(a, threads * V);
+  row_kernel<T, V, VPT, MODE, false><<<dim3((unsigned)a.tokens, batch), threads, 0, s>>>(a);
 }
 
 // A row of up to 256 vectors is a warp's, so that it needs no barrier; longer ones take the block that holds them with
@@ -455,17 +550,15 @@ cudaError_t launch_rows(bool bf16, const RowArgs& a, cudaStream_t s) {
 cudaError_t launch_rms_norm(bool bf16, long long rows, int width, const void* x, long long x_stride,
                             const void* residual, long long r_stride, const void* weight, float eps, void* sum_out,
                             long long sum_stride, void* out, long long out_stride, float* scale, cudaStream_t s) {
-  const RowArgs a{x, residual, weight, sum_out, out, scale, rows, width, width, -1, (int)rows,
-                  0, 0, x_stride, r_stride, sum_stride, out_stride, eps};
+  const RowArgs a{x, residual, weight, sum_out, out, scale, rows, width, width, (int)rows,
+                  0, 0, x_stride, r_stride, sum_stride, out_stride, eps, 1.f / (float)width, 0};
   return scale ? launch_rows<kNormI8>(bf16, a, s) : launch_rows<kNorm>(bf16, a, s);
 }
 
 cudaError_t launch_quantize_i8(bool bf16, int B, int H, int N, int d, const void* x, const da_head_strides& xs,
                                int8_t* q, long long q_stride, float* scale, cudaStream_t s) {
-  int shift = 0;
-  while ((1 << shift) < d) ++shift;
-  const RowArgs a{x, nullptr, nullptr, nullptr, q, scale, (long long)B * N, H * d, d, H == 1 ? 30 : (1 << shift) == d ? shift : -1, N,
-                  xs.batch, xs.head, xs.token, 0, 0, q_stride, 0.f};
+  const RowArgs a{x, nullptr, nullptr, nullptr, q, scale, (long long)B * N, H * d, d, N,
+                  xs.batch, xs.head, xs.token, 0, 0, q_stride, 0.f, 1.f, 0};
   return launch_rows<kQuantI8>(bf16, a, s);
 }
 

@@ -10,10 +10,10 @@
 //
 // The kernel is bound by HBM: x is read once and out written once.  A thread's unit of work is two
 // 16-byte vectors of a head, elements [j, j + V) and [j + d/2, j + d/2 + V): whole pairs in either pairing.
-// A group of threads owns a token, all its heads, in registers (the norm over all heads needs them
-// together); every unit of a thread has the same j, so its cosines and sines are loaded from shared memory
-// once a token.  A block takes a run of tokens: all its threads form the angles of the whole run first, behind
-// the loads of the first token, and each token's loads are issued before the one in front is worked on.
+// A group of threads owns a token, all its heads (the norm over all heads needs them together); every unit of a
+// thread has the same j, so its cosines and sines are loaded from shared memory once a token.  A group takes a run
+// of tokens: the block forms the angles of all of them first, and each thread keeps the loads of the next kStages tokens
+// in flight with cp.async, into shared memory that only it reads: loads ahead cost no registers and need no barrier.
 #include <math.h>
 
 #include "da_common.cuh"
@@ -25,6 +25,7 @@ namespace {
 
 constexpr int kMaxPairs = 64;   // d <= 128
 constexpr int kMaxRun = 32;     // tokens of a block
+constexpr int kStages = 3;      // tokens a thread holds in flight
 
 enum { kNoNorm = 0, kHeadNorm = 1, kFullNorm = 2 };
 
@@ -41,7 +42,7 @@ struct RopeArgs {
   long long xb, xh, xn, ob, oh, on;
   int grid[3];
   int norm, halves;
-  float eps;
+  float eps, inv_width;        // 1 / (H d)
   double freq[kMaxPairs];      // frequency / pi: half turns per position
   unsigned char axis[kMaxPairs];
 };
@@ -80,8 +81,11 @@ template <typename T, int D, int UPT>
 __global__ void __launch_bounds__(512) rope_kernel(const __grid_constant__ RopeArgs a) {
   constexpr int V = Vec<T>::n;
   constexpr int kPerHead = D / 2 / V;   // units of a head
+  extern __shared__ __align__(16) uint4 s_ring[];   // [stage][unit][vector][thread]
   __shared__ __align__(16) float s_cos[kMaxRun * D / 2], s_sin[kMaxRun * D / 2];
-  __shared__ bool s_turn[kMaxRun];
+  __shared__ int4 s_pos[kMaxRun];   // time, height, width, whether the token turns at all
+  __shared__ double s_freq[D / 2];
+  __shared__ unsigned char s_axis[D / 2];
   __shared__ float s_part[2][16];
   const int b = blockIdx.y, n0 = blockIdx.x * a.run, h0 = blockIdx.z * a.heads_per_block;
   const int run = min(a.run, a.N - n0);
@@ -91,58 +95,92 @@ __global__ void __launch_bounds__(512) rope_kernel(const __grid_constant__ RopeA
   const int j = (gt % kPerHead) * V;    // the same for all units of a thread: group is a multiple of kPerHead
   const T* x = static_cast<const T*>(a.x) + b * a.xb + (long long)h0 * a.xh + j;
   T* out = static_cast<T*>(a.out) + b * a.ob + (long long)h0 * a.oh + j;
-  const T* weight = static_cast<const T*>(a.weight) + j;
 
-  uint4 raw[UPT][2], next[UPT][2];
-  auto load = [&](int k, uint4 (&r)[UPT][2]) {
-    const T* p = x + (long long)(n0 + k) * a.xn;
+  auto slot = [&](int it, int i, int q) { return s_ring + ((it % kStages * UPT + i) * 2 + q) * blockDim.x + threadIdx.x; };
+  auto fetch = [&](int it) {   // token g + it * groups of the run
+    const int k = g + it * groups;
+    if (k < run) {
+      const T* p = x + (long long)(n0 + k) * a.xn;
 #pragma unroll
-    for (int i = 0; i < UPT; ++i) {
-      const int u = gt + i * a.group;
-      r[i][0] = r[i][1] = make_uint4(0, 0, 0, 0);
-      if (u < units && k < run) {
-        const T* e = p + (u / kPerHead) * a.xh;
-        r[i][0] = *reinterpret_cast<const uint4*>(e);
-        r[i][1] = *reinterpret_cast<const uint4*>(e + D / 2);
+      for (int i = 0; i < UPT; ++i) {
+        const int u = gt + i * a.group;
+        if (u < units) {
+          const T* e = p + (u / kPerHead) * a.xh;
+          cp_async16(slot(it, i, 0), e);
+          cp_async16(slot(it, i, 1), e + D / 2);
+        }
       }
     }
+    cp_async_commit();
   };
-  load(g, raw);
+#pragma unroll
+  for (int it = 0; it < kStages; ++it) fetch(it);
 
-  for (int i = threadIdx.x; i < run * (D / 2); i += blockDim.x) {
-    const int k = i / (D / 2), p = i % (D / 2), u = a.axis[p];
-    const unsigned n = (unsigned)(n0 + k);
-    int pos;
-    bool turn = true;
-    if (a.positions) {
-      pos = a.positions[b * a.pos_batch + (long long)n * 3 + u];
-    } else {
-      const unsigned row = n / (unsigned)a.grid[2], t = row / (unsigned)a.grid[1];
-      pos = (int)(u == 0 ? t : u == 1 ? row - t * a.grid[1] : n - row * a.grid[2]);
-      turn = t < (unsigned)a.grid[0];
+  // weights of the thread's units, the same for every token
+  uint4 wraw[UPT][2];
+#pragma unroll
+  for (int i = 0; i < UPT; ++i) {
+    const int u = gt + i * a.group;
+    wraw[i][0] = wraw[i][1] = make_uint4(0, 0, 0, 0);
+    if (a.norm != kNoNorm && u < units) {
+      const T* w = static_cast<const T*>(a.weight) + j + (a.norm == kFullNorm ? u / kPerHead * D : 0);
+      wraw[i][0] = *reinterpret_cast<const uint4*>(w);
+      wraw[i][1] = *reinterpret_cast<const uint4*>(w + D / 2);
     }
-    double half_turns = (double)pos * a.freq[p];
+  }
+
+  // positions of the run's tokens, and the frequencies out of the launch's constants (a warp reads those one at a time)
+  for (int k = threadIdx.x; k < run; k += blockDim.x) {
+    const unsigned n = (unsigned)(n0 + k);
+    if (a.positions) {
+      const int* pos = a.positions + b * a.pos_batch + (long long)n * 3;
+      s_pos[k] = make_int4(pos[0], pos[1], pos[2], 1);
+    } else {
+      const unsigned line = n / (unsigned)a.grid[2], t = line / (unsigned)a.grid[1];
+      s_pos[k] = make_int4((int)t, (int)(line - t * a.grid[1]), (int)(n - line * a.grid[2]), t < (unsigned)a.grid[0]);
+    }
+  }
+  for (int p = threadIdx.x; p < D / 2; p += blockDim.x) {
+    s_freq[p] = a.freq[p];
+    s_axis[p] = a.axis[p];
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < run * (D / 2); i += blockDim.x) {
+    const int p = i % (D / 2);
+    const int pos = reinterpret_cast<const int*>(&s_pos[i / (D / 2)])[s_axis[p]];
+    double half_turns = (double)pos * s_freq[p];
     half_turns -= 2.0 * rint(half_turns * 0.5);
     sincospif((float)half_turns, &s_sin[i], &s_cos[i]);
-    if (p == 0) s_turn[k] = turn;
   }
   __syncthreads();
 
   // every group takes the same number of turns, so that the barriers match
   for (int k0 = 0, it = 0; k0 < run; k0 += groups, ++it) {
     const int k = k0 + g;
-    const bool more = k0 + groups < run;
-    if (more) load(k + groups, next);
-    float v[UPT][2][V];
+    uint4 raw[UPT][2];
     float ss = 0.f, factor[UPT];
+    cp_async_wait<kStages - 1>();
 #pragma unroll
     for (int i = 0; i < UPT; ++i) {
-      Vec<T>::unpack(raw[i][0], v[i][0]);
-      Vec<T>::unpack(raw[i][1], v[i][1]);
+      const bool mine = k < run && gt + i * a.group < units;
+      raw[i][0] = mine ? *slot(it, i, 0) : make_uint4(0, 0, 0, 0);
+      raw[i][1] = mine ? *slot(it, i, 1) : make_uint4(0, 0, 0, 0);
       factor[i] = 0.f;
       if (a.norm != kNoNorm) {
+        uint64_t s2 = 0;
 #pragma unroll
-        for (int e = 0; e < V; ++e) factor[i] = fmaf(v[i][0][e], v[i][0][e], fmaf(v[i][1][e], v[i][1][e], factor[i]));
+        for (int q = 0; q < 2; ++q) {
+          float v[V];
+          Vec<T>::unpack(raw[i][q], v);
+#pragma unroll
+          for (int e = 0; e < V; e += 2) {
+            const uint64_t p2 = f2_pack(v[e], v[e + 1]);
+            s2 = f2_fma(p2, p2, s2);
+          }
+        }
+        float lo, hi;
+        f2_unpack(s2, lo, hi);
+        factor[i] = lo + hi;
         ss += factor[i];
       }
     }
@@ -163,13 +201,13 @@ __global__ void __launch_bounds__(512) rope_kernel(const __grid_constant__ RopeA
         for (int o = 8; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
         ss = __shfl_sync(0xffffffffu, ss, 0);
       }
-      const float f = rsqrtf(ss / (float)(a.H * D) + a.eps);
+      const float f = rsqrtf(ss * a.inv_width + a.eps);
 #pragma unroll
       for (int i = 0; i < UPT; ++i) factor[i] = f;
     }
     if (k < run) {
       T* o = out + (long long)(n0 + k) * a.on;
-      const bool turn = s_turn[k];
+      const bool turn = s_pos[k].w != 0;
       __align__(16) float c[V], s[V];   // halves: pairs j .. j + V; adjacent: V / 2 pairs of each vector
 #pragma unroll
       for (int q = 0; q < V; q += 4) {
@@ -189,47 +227,57 @@ __global__ void __launch_bounds__(512) rope_kernel(const __grid_constant__ RopeA
         const int u = gt + i * a.group;
         if (u >= units) continue;
         const int h = u / kPerHead;
+        float v[2][V];
+        Vec<T>::unpack(raw[i][0], v[0]);
+        Vec<T>::unpack(raw[i][1], v[1]);
         if (a.norm != kNoNorm) {
-          const T* w = weight + (a.norm == kFullNorm ? h * D : 0);
+          const uint64_t f2 = f2_pack(factor[i], factor[i]);
 #pragma unroll
           for (int q = 0; q < 2; ++q) {
             float wv[V];
-            Vec<T>::unpack(*reinterpret_cast<const uint4*>(w + q * (D / 2)), wv);
+            Vec<T>::unpack(wraw[i][q], wv);
 #pragma unroll
-            for (int e = 0; e < V; ++e) v[i][q][e] *= factor[i] * wv[e];
+            for (int e = 0; e < V; e += 2)
+              f2_unpack(f2_mul(f2_mul(f2_pack(v[q][e], v[q][e + 1]), f2), f2_pack(wv[e], wv[e + 1])), v[q][e], v[q][e + 1]);
           }
         }
         if (turn) {   // a token that does not turn is copied, whatever it holds
           if (a.halves) {
 #pragma unroll
             for (int e = 0; e < V; ++e) {
-              const float va = v[i][0][e], vb = v[i][1][e];
-              v[i][0][e] = va * c[e] - vb * s[e];
-              v[i][1][e] = va * s[e] + vb * c[e];
+              const float va = v[0][e], vb = v[1][e];
+              v[0][e] = va * c[e] - vb * s[e];
+              v[1][e] = va * s[e] + vb * c[e];
             }
           } else {
 #pragma unroll
             for (int q = 0; q < 2; ++q)
 #pragma unroll
               for (int e = 0; e < V / 2; ++e) {
-                const float va = v[i][q][2 * e], vb = v[i][q][2 * e + 1];
+                const float va = v[q][2 * e], vb = v[q][2 * e + 1];
                 const float ce = c[q * (V / 2) + e], se = s[q * (V / 2) + e];
-                v[i][q][2 * e] = va * ce - vb * se;
-                v[i][q][2 * e + 1] = va * se + vb * ce;
+                v[q][2 * e] = va * ce - vb * se;
+                v[q][2 * e + 1] = va * se + vb * ce;
               }
           }
         }
         T* e = o + (long long)h * a.oh;
-        *reinterpret_cast<uint4*>(e) = Vec<T>::pack(v[i][0]);
-        *reinterpret_cast<uint4*>(e + D / 2) = Vec<T>::pack(v[i][1]);
+        *reinterpret_cast<uint4*>(e) = Vec<T>::pack(v[0]);
+        *reinterpret_cast<uint4*>(e + D / 2) = Vec<T>::pack(v[1]);
       }
     }
-#pragma unroll
-    for (int i = 0; i < UPT; ++i) {
-      raw[i][0] = next[i][0];
-      raw[i][1] = next[i][1];
-    }
+    fetch(it + kStages);   // into the slots that this turn has read
   }
+}
+
+template <typename T, int D, int UPT>
+cudaError_t launch_units(const RopeArgs& a, dim3 grid, int threads, cudaStream_t s) {
+  auto kernel = rope_kernel<T, D, UPT>;
+  const size_t ring = (size_t)kStages * UPT * 2 * threads * 16;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)ring);
+  if (e != cudaSuccess) return e;
+  kernel<<<grid, threads, ring, s>>>(a);
+  return cudaGetLastError();
 }
 
 template <typename T, int D>
@@ -249,17 +297,17 @@ cudaError_t launch_typed(RopeArgs& a, int B, cudaStream_t s) {
     threads = a.group = ((units + upt - 1) / upt + 31) / 32 * 32;
   }
   const int groups = threads / a.group;
-  // run: long enough to spread the angles over the threads, short enough for the blocks to fill the GPU
+  // run: long enough to spread the angles over the threads and to keep loads ahead, short enough for the blocks to
+  // fill the GPU several times over
   const long long tokens = (long long)B * a.N;
   int per_group = 1;
   while (per_group < 8 && groups * per_group * 2 <= kMaxRun && tokens / (groups * per_group * 2) >= 148 * 16) per_group *= 2;
   a.run = groups * per_group;
   const dim3 grid((unsigned)((a.N + a.run - 1) / a.run), (unsigned)B, (unsigned)((a.H + a.heads_per_block - 1) / a.heads_per_block));
-  if (upt == 1) rope_kernel<T, D, 1><<<grid, threads, 0, s>>>(a);
-  else if (upt == 2) rope_kernel<T, D, 2><<<grid, threads, 0, s>>>(a);
-  else if (upt == 3) rope_kernel<T, D, 3><<<grid, threads, 0, s>>>(a);
-  else rope_kernel<T, D, 4><<<grid, threads, 0, s>>>(a);
-  return cudaGetLastError();
+  return upt == 1   ? launch_units<T, D, 1>(a, grid, threads, s)
+         : upt == 2 ? launch_units<T, D, 2>(a, grid, threads, s)
+         : upt == 3 ? launch_units<T, D, 3>(a, grid, threads, s)
+                    : launch_units<T, D, 4>(a, grid, threads, s);
 }
 
 }  // namespace
@@ -280,6 +328,7 @@ cudaError_t launch_rope(bool bf16, const da_rope_plan& plan, int B, int H, int N
   for (int u = 0; u < 3; ++u) a.grid[u] = plan.grid[u];
   a.norm = !weight ? kNoNorm : weight_width == d ? kHeadNorm : kFullNorm;
   a.eps = eps;
+  a.inv_width = 1.f / ((float)H * (float)d);
   a.halves = plan.pairing == DA_ROPE_HALVES;
   int p = 0;
   for (int u = 0; u < 3; ++u)

@@ -47,11 +47,6 @@ constexpr float kSplit = 65.f;
 template <int MODE>
 constexpr float kNear = MODE == kQuantI8 ? 1.52587891e-5f : 6.10351562e-5f;
 
-__device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
 __device__ __forceinline__ float max3_nan(float a, float b, float c) {   // a NaN wins over every number
   float r;
   asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));

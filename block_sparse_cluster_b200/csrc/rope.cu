@@ -47,42 +47,109 @@ struct RopeArgs {
   unsigned char axis[kMaxPairs];
 };
 
-template <typename T>
-struct Vec;   // 16 bytes
-template <>
-struct Vec<__nv_bfloat16> {
+// A unit's two raw vectors as V pairs: a[i] and b[i] hold the first and second elements of pairs 2i and 2i + 1, so that
+// the rotation works on two pairs an instruction in either pairing.
+template <typename T, bool HALVES>
+struct Unit;
+
+// (a, b) -> (a c - b s, a s + b c), two pairs at a time
+template <int N>
+__device__ __forceinline__ void rotate_pairs(uint64_t (&a)[N], uint64_t (&b)[N], const uint64_t (&c)[N], const uint64_t (&s)[N]) {
+#pragma unroll
+  for (int e = 0; e < N; ++e) {
+    const uint64_t t = a[e];
+    a[e] = f2_fma(t, c[e], f2_mul(b[e], s[e] ^ 0x8000000080000000ull));
+    b[e] = f2_fma(t, s[e], f2_mul(b[e], c[e]));
+  }
+}
+template <bool HALVES>
+struct Unit<__nv_bfloat16, HALVES> {
   static constexpr int n = 8;
-  static __device__ __forceinline__ void unpack(const uint4& raw, float* o) {
-    const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+  static __device__ __forceinline__ uint64_t low(uint32_t p, uint32_t q) {
+    return f2_pack(__uint_as_float(p << 16), __uint_as_float(q << 16));
+  }
+  static __device__ __forceinline__ uint64_t high(uint32_t p, uint32_t q) {
+    return f2_pack(__uint_as_float(p & 0xffff0000u), __uint_as_float(q & 0xffff0000u));
+  }
+  static __device__ __forceinline__ void unpack(const uint4 (&raw)[2], uint64_t (&a)[4], uint64_t (&b)[4]) {
+    const uint32_t w[2][4] = {{raw[0].x, raw[0].y, raw[0].z, raw[0].w}, {raw[1].x, raw[1].y, raw[1].z, raw[1].w}};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      o[2 * i] = __uint_as_float(w[i] << 16);
-      o[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+      if (HALVES) {
+        a[i] = f2_pack(__uint_as_float(w[0][i] << 16), __uint_as_float(w[0][i] & 0xffff0000u));
+        b[i] = f2_pack(__uint_as_float(w[1][i] << 16), __uint_as_float(w[1][i] & 0xffff0000u));
+      } else {
+        a[i] = low(w[i / 2][2 * (i & 1)], w[i / 2][2 * (i & 1) + 1]);
+        b[i] = high(w[i / 2][2 * (i & 1)], w[i / 2][2 * (i & 1) + 1]);
+      }
     }
   }
-  static __device__ __forceinline__ uint4 pack(const float* v) {
-    return make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+  static __device__ __forceinline__ void rotate(uint64_t (&a)[4], uint64_t (&b)[4], const uint64_t (&c)[4], const uint64_t (&s)[4]) {
+    rotate_pairs(a, b, c, s);
+  }
+  static __device__ __forceinline__ void pack(const uint64_t (&a)[4], const uint64_t (&b)[4], uint4 (&raw)[2]) {
+    uint32_t w[2][4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float a0, a1, b0, b1;
+      f2_unpack(a[i], a0, a1);
+      f2_unpack(b[i], b0, b1);
+      if (HALVES) {
+        w[0][i] = pack_bf16x2(a0, a1);
+        w[1][i] = pack_bf16x2(b0, b1);
+      } else {
+        w[i / 2][2 * (i & 1)] = pack_bf16x2(a0, b0);
+        w[i / 2][2 * (i & 1) + 1] = pack_bf16x2(a1, b1);
+      }
+    }
+    raw[0] = make_uint4(w[0][0], w[0][1], w[0][2], w[0][3]);
+    raw[1] = make_uint4(w[1][0], w[1][1], w[1][2], w[1][3]);
   }
 };
-template <>
-struct Vec<float> {
+// fp32 vectors are taken as they lie: with adjacent pairs a[i] and b[i] are whole pairs of the first and second vector,
+// and the rotation takes them apart (picking firsts and seconds together would cost moves; it was 10 % slower).
+template <bool HALVES>
+struct Unit<float, HALVES> {
   static constexpr int n = 4;
-  static __device__ __forceinline__ void unpack(const uint4& raw, float* o) {
-    o[0] = __uint_as_float(raw.x); o[1] = __uint_as_float(raw.y);
-    o[2] = __uint_as_float(raw.z); o[3] = __uint_as_float(raw.w);
+  static __device__ __forceinline__ uint64_t two(uint32_t p, uint32_t q) { return f2_pack(__uint_as_float(p), __uint_as_float(q)); }
+  static __device__ __forceinline__ void unpack(const uint4 (&raw)[2], uint64_t (&a)[2], uint64_t (&b)[2]) {
+    a[0] = two(raw[0].x, raw[0].y); a[1] = two(raw[0].z, raw[0].w);
+    b[0] = two(raw[1].x, raw[1].y); b[1] = two(raw[1].z, raw[1].w);
   }
-  static __device__ __forceinline__ uint4 pack(const float* v) {
-    return make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+  static __device__ __forceinline__ uint64_t turn(uint64_t v, float c, float s) {
+    float p, q;
+    f2_unpack(v, p, q);
+    return f2_pack(p * c - q * s, p * s + q * c);
+  }
+  static __device__ __forceinline__ void rotate(uint64_t (&a)[2], uint64_t (&b)[2], const uint64_t (&c)[2], const uint64_t (&s)[2]) {
+    if (HALVES) {
+      rotate_pairs(a, b, c, s);
+    } else {
+      float cs[4], sn[4];
+      f2_unpack(c[0], cs[0], cs[1]); f2_unpack(c[1], cs[2], cs[3]);
+      f2_unpack(s[0], sn[0], sn[1]); f2_unpack(s[1], sn[2], sn[3]);
+      a[0] = turn(a[0], cs[0], sn[0]); a[1] = turn(a[1], cs[1], sn[1]);
+      b[0] = turn(b[0], cs[2], sn[2]); b[1] = turn(b[1], cs[3], sn[3]);
+    }
+  }
+  static __device__ __forceinline__ void pack(const uint64_t (&a)[2], const uint64_t (&b)[2], uint4 (&raw)[2]) {
+    float v[8];
+    f2_unpack(a[0], v[0], v[1]); f2_unpack(a[1], v[2], v[3]);
+    f2_unpack(b[0], v[4], v[5]); f2_unpack(b[1], v[6], v[7]);
+    raw[0] = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+    raw[1] = make_uint4(__float_as_uint(v[4]), __float_as_uint(v[5]), __float_as_uint(v[6]), __float_as_uint(v[7]));
   }
 };
 
 // UPT: units a thread holds of a token.
-template <typename T, int D, int UPT>
-__global__ void __launch_bounds__(512) rope_kernel(const __grid_constant__ RopeArgs a) {
-  constexpr int V = Vec<T>::n;
+template <typename T, int D, int UPT, bool HALVES, bool NORMED>
+__global__ void __launch_bounds__(512, UPT == 1 ? 2 : 1) rope_kernel(const __grid_constant__ RopeArgs a) {
+  using U = Unit<T, HALVES>;
+  constexpr int V = U::n;
   constexpr int kPerHead = D / 2 / V;   // units of a head
   extern __shared__ __align__(16) uint4 s_ring[];   // [stage][unit][vector][thread]
-  __shared__ __align__(16) float s_cos[kMaxRun * D / 2], s_sin[kMaxRun * D / 2];
+  float* const s_cos = reinterpret_cast<float*>(s_ring + kStages * UPT * 2 * blockDim.x);   // [token of the run][pair]
+  float* const s_sin = s_cos + a.run * (D / 2);
   __shared__ int4 s_pos[kMaxRun];   // time, height, width, whether the token turns at all
   __shared__ double s_freq[D / 2];
   __shared__ unsigned char s_axis[D / 2];
@@ -117,15 +184,17 @@ __global__ void __launch_bounds__(512) rope_kernel(const __grid_constant__ RopeA
   for (int it = 0; it < kStages; ++it) fetch(it);
 
   // weights of the thread's units, the same for every token
-  uint4 wraw[UPT][2];
+  uint4 wraw[NORMED ? UPT : 1][2];
+  if (NORMED) {
 #pragma unroll
-  for (int i = 0; i < UPT; ++i) {
-    const int u = gt + i * a.group;
-    wraw[i][0] = wraw[i][1] = make_uint4(0, 0, 0, 0);
-    if (a.norm != kNoNorm && u < units) {
-      const T* w = static_cast<const T*>(a.weight) + j + (a.norm == kFullNorm ? u / kPerHead * D : 0);
-      wraw[i][0] = *reinterpret_cast<const uint4*>(w);
-      wraw[i][1] = *reinterpret_cast<const uint4*>(w + D / 2);
+    for (int i = 0; i < UPT; ++i) {
+      const int u = gt + i * a.group;
+      wraw[i][0] = wraw[i][1] = make_uint4(0, 0, 0, 0);
+      if (u < units) {
+        const T* w = static_cast<const T*>(a.weight) + j + (a.norm == kFullNorm ? u / kPerHead * D : 0);
+        wraw[i][0] = *reinterpret_cast<const uint4*>(w);
+        wraw[i][1] = *reinterpret_cast<const uint4*>(w + D / 2);
+      }
     }
   }
 
@@ -165,33 +234,26 @@ __global__ void __launch_bounds__(512) rope_kernel(const __grid_constant__ RopeA
       const bool mine = k < run && gt + i * a.group < units;
       raw[i][0] = mine ? *slot(it, i, 0) : make_uint4(0, 0, 0, 0);
       raw[i][1] = mine ? *slot(it, i, 1) : make_uint4(0, 0, 0, 0);
-      factor[i] = 0.f;
-      if (a.norm != kNoNorm) {
-        uint64_t s2 = 0;
+      factor[i] = 1.f;
+      if (NORMED) {
+        uint64_t va[V / 2], vb[V / 2], s2 = 0;
+        U::unpack(raw[i], va, vb);
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          float v[V];
-          Vec<T>::unpack(raw[i][q], v);
-#pragma unroll
-          for (int e = 0; e < V; e += 2) {
-            const uint64_t p2 = f2_pack(v[e], v[e + 1]);
-            s2 = f2_fma(p2, p2, s2);
-          }
-        }
+        for (int e = 0; e < V / 2; ++e) s2 = f2_fma(va[e], va[e], f2_fma(vb[e], vb[e], s2));
         float lo, hi;
         f2_unpack(s2, lo, hi);
         factor[i] = lo + hi;
         ss += factor[i];
       }
     }
-    if (a.norm == kHeadNorm) {
+    if (NORMED && a.norm == kHeadNorm) {
 #pragma unroll
       for (int i = 0; i < UPT; ++i) {
 #pragma unroll
         for (int o = kPerHead / 2; o > 0; o >>= 1) factor[i] += __shfl_xor_sync(0xffffffffu, factor[i], o);
         factor[i] = rsqrtf(factor[i] * (1.f / D) + a.eps);
       }
-    } else if (a.norm == kFullNorm) {
+    } else if (NORMED) {
       for (int o = min(a.group, 32) / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
       if (a.group > 32) {
         if ((threadIdx.x & 31) == 0) s_part[it & 1][threadIdx.x >> 5] = ss;
@@ -208,62 +270,42 @@ __global__ void __launch_bounds__(512) rope_kernel(const __grid_constant__ RopeA
     if (k < run) {
       T* o = out + (long long)(n0 + k) * a.on;
       const bool turn = s_pos[k].w != 0;
-      __align__(16) float c[V], s[V];   // halves: pairs j .. j + V; adjacent: V / 2 pairs of each vector
+      // halves: pairs j .. j + V; adjacent: V / 2 pairs of each vector
+      uint64_t c[V / 2], s[V / 2];
 #pragma unroll
-      for (int q = 0; q < V; q += 4) {
-        const int at = k * (D / 2) + (a.halves ? j + q : q < V / 2 ? j / 2 + q : j / 2 + D / 4 + q - V / 2);
-        if (V == 8 || a.halves) {
-          *reinterpret_cast<float4*>(&c[q]) = *reinterpret_cast<const float4*>(s_cos + at);
-          *reinterpret_cast<float4*>(&s[q]) = *reinterpret_cast<const float4*>(s_sin + at);
-        } else {   // V = 4, adjacent: two pairs of each vector
-          *reinterpret_cast<float2*>(&c[0]) = *reinterpret_cast<const float2*>(s_cos + at);
-          *reinterpret_cast<float2*>(&s[0]) = *reinterpret_cast<const float2*>(s_sin + at);
-          *reinterpret_cast<float2*>(&c[2]) = *reinterpret_cast<const float2*>(s_cos + at + D / 4);
-          *reinterpret_cast<float2*>(&s[2]) = *reinterpret_cast<const float2*>(s_sin + at + D / 4);
+      for (int q = 0; q < 2; ++q) {
+        const int at = k * (D / 2) + (HALVES ? j + q * (V / 2) : j / 2 + q * (D / 4));
+        if (V == 8) {
+          const ulonglong2 cq = *reinterpret_cast<const ulonglong2*>(s_cos + at), sq = *reinterpret_cast<const ulonglong2*>(s_sin + at);
+          c[2 * q] = cq.x; c[(2 * q + 1) % (V / 2)] = cq.y;
+          s[2 * q] = sq.x; s[(2 * q + 1) % (V / 2)] = sq.y;
+        } else {
+          c[q] = *reinterpret_cast<const uint64_t*>(s_cos + at);
+          s[q] = *reinterpret_cast<const uint64_t*>(s_sin + at);
         }
       }
 #pragma unroll
       for (int i = 0; i < UPT; ++i) {
         const int u = gt + i * a.group;
         if (u >= units) continue;
-        const int h = u / kPerHead;
-        float v[2][V];
-        Vec<T>::unpack(raw[i][0], v[0]);
-        Vec<T>::unpack(raw[i][1], v[1]);
-        if (a.norm != kNoNorm) {
+        uint64_t va[V / 2], vb[V / 2];
+        U::unpack(raw[i], va, vb);
+        if (NORMED) {
+          uint64_t wa[V / 2], wb[V / 2];
+          U::unpack(wraw[i], wa, wb);
           const uint64_t f2 = f2_pack(factor[i], factor[i]);
 #pragma unroll
-          for (int q = 0; q < 2; ++q) {
-            float wv[V];
-            Vec<T>::unpack(wraw[i][q], wv);
-#pragma unroll
-            for (int e = 0; e < V; e += 2)
-              f2_unpack(f2_mul(f2_mul(f2_pack(v[q][e], v[q][e + 1]), f2), f2_pack(wv[e], wv[e + 1])), v[q][e], v[q][e + 1]);
+          for (int e = 0; e < V / 2; ++e) {
+            va[e] = f2_mul(va[e], f2_mul(wa[e], f2));
+            vb[e] = f2_mul(vb[e], f2_mul(wb[e], f2));
           }
         }
-        if (turn) {   // a token that does not turn is copied, whatever it holds
-          if (a.halves) {
-#pragma unroll
-            for (int e = 0; e < V; ++e) {
-              const float va = v[0][e], vb = v[1][e];
-              v[0][e] = va * c[e] - vb * s[e];
-              v[1][e] = va * s[e] + vb * c[e];
-            }
-          } else {
-#pragma unroll
-            for (int q = 0; q < 2; ++q)
-#pragma unroll
-              for (int e = 0; e < V / 2; ++e) {
-                const float va = v[q][2 * e], vb = v[q][2 * e + 1];
-                const float ce = c[q * (V / 2) + e], se = s[q * (V / 2) + e];
-                v[q][2 * e] = va * ce - vb * se;
-                v[q][2 * e + 1] = va * se + vb * ce;
-              }
-          }
-        }
-        T* e = o + (long long)h * a.oh;
-        *reinterpret_cast<uint4*>(e) = Vec<T>::pack(v[0]);
-        *reinterpret_cast<uint4*>(e + D / 2) = Vec<T>::pack(v[1]);
+        if (turn) U::rotate(va, vb, c, s);   // a token that does not turn is copied, whatever it holds
+        uint4 o2[2];
+        U::pack(va, vb, o2);
+        T* e = o + (long long)(u / kPerHead) * a.oh;
+        *reinterpret_cast<uint4*>(e) = o2[0];
+        *reinterpret_cast<uint4*>(e + D / 2) = o2[1];
       }
     }
     fetch(it + kStages);   // into the slots that this turn has read
@@ -272,17 +314,18 @@ __global__ void __launch_bounds__(512) rope_kernel(const __grid_constant__ RopeA
 
 template <typename T, int D, int UPT>
 cudaError_t launch_units(const RopeArgs& a, dim3 grid, int threads, cudaStream_t s) {
-  auto kernel = rope_kernel<T, D, UPT>;
-  const size_t ring = (size_t)kStages * UPT * 2 * threads * 16;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)ring);
+  auto kernel = a.halves ? (a.norm ? rope_kernel<T, D, UPT, true, true> : rope_kernel<T, D, UPT, true, false>)
+                         : (a.norm ? rope_kernel<T, D, UPT, false, true> : rope_kernel<T, D, UPT, false, false>);
+  const size_t smem = (size_t)kStages * UPT * 2 * threads * 16 + (size_t)a.run * D * 4;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  kernel<<<grid, threads, ring, s>>>(a);
+  kernel<<<grid, threads, smem, s>>>(a);
   return cudaGetLastError();
 }
 
 template <typename T, int D>
 cudaError_t launch_typed(RopeArgs& a, int B, cudaStream_t s) {
-  constexpr int kPerHead = D / 2 / Vec<T>::n;
+  constexpr int kPerHead = D / 2 * (int)sizeof(T) / 16;
   // without the norm over all heads a token's heads may go to several blocks
   a.heads_per_block = a.norm == kFullNorm ? a.H : (a.H < 1024 / kPerHead ? a.H : 1024 / kPerHead);
   const int units = a.heads_per_block * kPerHead;

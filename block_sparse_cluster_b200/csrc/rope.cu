@@ -330,13 +330,17 @@ cudaError_t launch_typed(RopeArgs& a, int B, cudaStream_t s) {
   a.heads_per_block = a.norm == kFullNorm ? a.H : (a.H < 1024 / kPerHead ? a.H : 1024 / kPerHead);
   const int units = a.heads_per_block * kPerHead;
   int threads, upt;
-  if (units <= 128) {   // a warp, or less, a token
+  // Few units: a warp, or less, a token, so that a sum stays in it; the norm's weights leave room for two units a thread.
+  // More: a block a token, one unit a thread while that fills few warps, since registers are what bounds the warps of an
+  // SM (bf16, 12 heads of 128, head norm: 40 us against 45 with three units in a warp; 16 heads: 79 against 158), two or
+  // four where the barrier of the norm over all heads would join many warps (40 heads: 269 us against 296 with one).
+  if (units <= (a.norm == kNoNorm ? 128 : 64)) {
     a.group = kPerHead;
     while (a.group < units && a.group < 32) a.group *= 2;
     upt = (units + 31) / 32;
     threads = 128;
   } else {
-    upt = units <= 1024 ? 2 : 4;
+    upt = units <= (a.norm == kFullNorm ? 256 : 512) ? 1 : units <= 1024 ? 2 : 4;
     threads = a.group = ((units + upt - 1) / upt + 31) / 32 * 32;
   }
   const int groups = threads / a.group;

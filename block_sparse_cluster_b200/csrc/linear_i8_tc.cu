@@ -14,8 +14,12 @@
 //              head), while the next tile's products fill the other accumulator.
 //
 // Two forms.  Pair (kPair): two CTAs of a cluster form a 256 x 256 tile with cta_group::2; each loads its
-// own 128 rows of x and half of the w rows, so every loaded byte serves 256 rows or columns.  Single:
-// one CTA forms 128 x kN.
+// own 128 rows of x and half of the w rows, so every loaded byte serves 256 rows or columns.  Single: one CTA forms 128 x n,
+// n any multiple of 16 up to 256, so that the tiles of a small product can be cut to fill the GPU (choose_tile).
+//
+// A product of few rows is bound by the loads of w, and the waits of the ring would bound it first: then a stage
+// holds up to four slices of depth, and only as many rows of x as there are.  The tensor core still reads 128 rows: the ones
+// beyond are whatever lies behind in the block's shared memory, and their products are never stored.
 #include "da_common.cuh"
 #include "da_internal.h"
 #include "tma_host.h"
@@ -30,29 +34,42 @@ constexpr int kThreads = 256;
 constexpr int kABytes = kTileM * kBlockK;    // 16 KB
 constexpr int kGroupM = 8;                   // row tiles that are walked together for each column tile
 
-template <bool kPair, int kN>
-struct Cfg {
-  static constexpr int kBRows = kPair ? kN / 2 : kN;      // w rows a CTA loads
-  static constexpr int kStageBytes = kABytes + kBRows * kBlockK;
-  static constexpr int kStages = kStageBytes >= 32768 ? 6 : 8;
-  static constexpr int kColumns = 2 * kN < 32 ? 32 : 2 * kN;   // tensor memory of two accumulators
-  static constexpr size_t kSmem = 1024 + (size_t)kStages * kStageBytes + 4 * 4096 /*staging*/ + 2 * 2 * kN * 4 /*scales, bias*/;
-};
+constexpr int kMaxN = 256;                   // columns of a tile
+constexpr int kMaxStages = 16;
+constexpr int kRingBytes = 6 * 32768;        // stages; 128 + 256 rows of a single CTA's tile fit four times
+constexpr int kStagingBytes = 4 * 4096;      // behind the ring, and at least the 16 KB that a short tile of x is read beyond it
+constexpr size_t kSmem = 1024 + kRingBytes + kStagingBytes + 2 * 2 * kMaxN * 4 /*scales, bias*/;
+static_assert(kStagingBytes >= kABytes, "a short tile of x is read as a whole one");
+static_assert(kSmem + 1024 <= 232448, "shared memory of one CTA per SM");
 
 struct Params {
   LinearArgs a;
-  int tiles_m, tiles_n, k_blocks, a_box_rows;
-  int vec;        // rows of the output can be stored 16 bytes at a time
+  int tiles_m, tiles_n, k_blocks;
+  int n;              // columns of a tile
+  int a_rows, b_rows; // rows of x and w that a CTA loads for a tile
+  int sub, stages;    // slices of a stage, stages of the ring
+  int vec;            // rows of the output can be stored 16 bytes at a time
   int* status;
 };
 
-template <int kStages>
 struct __align__(8) Bars {
-  uint64_t full[kStages], empty[kStages];
+  uint64_t full[kMaxStages], empty[kMaxStages];
   uint64_t acc_full[2], acc_empty[2];
   uint64_t drain;
   uint32_t tmem_base;
   int abort;
+};
+
+// Place in the ring: stage and the parity of its turn.
+struct Turn {
+  int s = 0;
+  uint32_t ph = 0;
+  __device__ __forceinline__ void next(int stages) {
+    if (++s == stages) {
+      s = 0;
+      ph ^= 1;
+    }
+  }
 };
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -146,18 +163,16 @@ __device__ __forceinline__ void tile_at(int t, const Params& p, int& tm, int& tn
 
 __device__ __forceinline__ void epilogue_barrier() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
 
-template <typename T, bool kPair, int kN>
+template <typename T, bool kPair>
 __global__ void __launch_bounds__(kThreads, 1)
 linear_i8_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w,
                     const __grid_constant__ Params p) {
-  using C = Cfg<kPair, kN>;
-  constexpr int kStages = C::kStages;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ Bars<kStages> bars;
+  __shared__ Bars bars;
   const uint32_t raw = smem_u32(smem_raw);
   uint8_t* ring = smem_raw + (((raw + 1023u) & ~1023u) - raw);
-  uint8_t* staging = ring + (size_t)kStages * C::kStageBytes;
-  float* s_cols = reinterpret_cast<float*>(staging + 4 * 4096);   // [2 tiles][scale, bias][kN]
+  uint8_t* staging = ring + kRingBytes;
+  float* s_cols = reinterpret_cast<float*>(staging + kStagingBytes);   // [2 tiles][scale, bias][kMaxN]
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = kPair ? cluster_rank() : 0;
@@ -165,10 +180,12 @@ linear_i8_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_const
   const int step = kPair ? gridDim.x >> 1 : gridDim.x;
   const int tiles = p.tiles_m * p.tiles_n;
   constexpr int kRowsPerTile = kPair ? 2 * kTileM : kTileM;
+  const int a_bytes = kPair ? kABytes : p.a_rows * kBlockK, slice_bytes = a_bytes + (kPair ? kABytes : p.b_rows * kBlockK);
+  const int sub = kPair ? 1 : p.sub, stages = kPair ? kRingBytes / (2 * kABytes) : p.stages;
   volatile int* abort = &bars.abort;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kStages; ++s) {
+    for (int s = 0; s < stages; ++s) {
       mbar_init(&bars.full[s], 1);
       mbar_init(&bars.empty[s], 1);
     }
@@ -180,7 +197,7 @@ linear_i8_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_const
     bars.abort = 0;
     fence_mbar_init();
   }
-  if (warp == 2) alloc_columns<kPair>(&bars.tmem_base, C::kColumns);
+  if (warp == 2) alloc_columns<kPair>(&bars.tmem_base, 2 * kMaxN);
   tc_fence_before();
   __syncthreads();
   if (kPair) cluster_sync();
@@ -191,47 +208,56 @@ linear_i8_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_const
     if (lane == 0) {
       tma_prefetch(&tm_x);
       tma_prefetch(&tm_w);
-      const uint32_t bytes = (uint32_t)(p.a_box_rows * kBlockK + C::kBRows * kBlockK) * (kPair ? 2u : 1u);
+      Turn turn;
       int it = 0;
       bool ok = true;
       for (int t = first; t < tiles && ok; t += step) {
         int tm, tn;
         tile_at(t, p, tm, tn);
         const int row = tm * kRowsPerTile + (int)rank * kTileM;
-        const int col = tn * kN + (int)rank * C::kBRows;
-        for (int kb = 0; kb < p.k_blocks; ++kb, ++it) {
-          const int s = it % kStages, ph = (it / kStages) & 1;
-          if (!mbar_wait(&bars.empty[s], ph ^ 1, abort, p.status)) { ok = false; break; }
-          uint8_t* a = ring + (size_t)s * C::kStageBytes;
+        const int col = tn * p.n + (int)rank * p.b_rows;
+        for (int kb = 0; kb < p.k_blocks; kb += sub, ++it, turn.next(stages)) {
+          const int s = turn.s, slices = kPair ? 1 : min(sub, p.k_blocks - kb);
+          if (!mbar_wait(&bars.empty[s], turn.ph ^ 1, abort, p.status)) { ok = false; break; }
+          uint8_t* a = ring + s * sub * slice_bytes;
           // a pair's copies all land on the leader's barrier, which expects the bytes of both
           const uint32_t bar = kPair ? map_to_rank(smem_u32(&bars.full[s]), 0) : smem_u32(&bars.full[s]);
-          if (rank == 0) mbar_expect_tx(&bars.full[s], bytes);
-          tma_load_2d<kPair>(a, &tm_x, bar, kb * kBlockK, row);
-          tma_load_2d<kPair>(a + kABytes, &tm_w, bar, kb * kBlockK, col);
+          if (rank == 0) mbar_expect_tx(&bars.full[s], (uint32_t)(slices * slice_bytes) * (kPair ? 2u : 1u));
+          for (int i = 0; i < slices; ++i, a += slice_bytes) {
+            tma_load_2d<kPair>(a, &tm_x, bar, (kb + i) * kBlockK, row);
+            tma_load_2d<kPair>(a + a_bytes, &tm_w, bar, (kb + i) * kBlockK, col);
+          }
         }
       }
       // given up: wait (within a limit) for the copies in flight before the block's memory goes
       if (!ok && rank == 0)
-        for (int i = max(0, it - kStages); i < it; ++i) mbar_wait_drain(&bars.full[i % kStages], (i / kStages) & 1);
+        for (int i = max(0, it - stages); i < it; ++i) mbar_wait_drain(&bars.full[i % stages], (i / stages) & 1);
     }
   } else if (warp == 1 && rank == 0) {
     if (lane == 0) {
-      const uint32_t idesc = idesc_i8(kRowsPerTile, kN);
-      int it = 0, n = 0;
+      const uint32_t idesc = idesc_i8(kRowsPerTile, kPair ? kMaxN : p.n);
+      const uint64_t desc0 = sdesc_sw128(smem_u32(ring), 16, 1024);
+      Turn turn;
+      int n = 0;
       bool ok = true;
       for (int t = first; t < tiles && ok; t += step, ++n) {
         const int b = n & 1;
         if (!mbar_wait(&bars.acc_empty[b], ((n >> 1) & 1) ^ 1, abort, p.status)) break;
         tc_fence_after();
-        for (int kb = 0; kb < p.k_blocks; ++kb, ++it) {
-          const int s = it % kStages, ph = (it / kStages) & 1;
-          if (!mbar_wait(&bars.full[s], ph, abort, p.status)) { ok = false; break; }
+        uint32_t accumulate = 0;
+        for (int kb = 0; kb < p.k_blocks; kb += sub, turn.next(stages)) {
+          const int s = turn.s, slices = kPair ? 1 : min(sub, p.k_blocks - kb);
+          if (!mbar_wait(&bars.full[s], turn.ph, abort, p.status)) { ok = false; break; }
           tc_fence_after();
-          const uint32_t a = smem_u32(ring + (size_t)s * C::kStageBytes);
+          // descriptors count addresses in 16 bytes
+          uint64_t ad = desc0 + (uint32_t)(s * sub * slice_bytes >> 4);
+          for (int i = 0; i < slices; ++i, ad += (uint32_t)(slice_bytes >> 4)) {
 #pragma unroll
-          for (int ks = 0; ks < kBlockK / 32; ++ks)
-            mma_i8<kPair>(tmem + b * kN, sdesc_sw128(a + ks * 32, 16, 1024), sdesc_sw128(a + kABytes + ks * 32, 16, 1024),
-                          idesc, (kb | ks) != 0);
+            for (int ks = 0; ks < kBlockK / 32; ++ks) {
+              mma_i8<kPair>(tmem + b * kMaxN, ad + 2 * ks, ad + (uint32_t)(a_bytes >> 4) + 2 * ks, idesc, accumulate);
+              accumulate = 1;
+            }
+          }
           mma_commit<kPair>(&bars.empty[s]);
         }
         if (ok) mma_commit<kPair>(&bars.acc_full[b]);
@@ -254,12 +280,12 @@ linear_i8_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_const
       int tm, tn;
       tile_at(t, p, tm, tn);
       const int b = n & 1;
-      const int n0 = tn * kN;
-      float* cs = s_cols + b * 2 * kN;
-      for (int i = threadIdx.x - 128; i < kN; i += 128) {
-        const bool in = n0 + i < A.N;
+      const int n0 = tn * p.n, n1 = min(n0 + p.n, A.N);   // the tile's columns
+      float* cs = s_cols + b * 2 * kMaxN;
+      for (int i = threadIdx.x - 128; i < kMaxN; i += 128) {
+        const bool in = n0 + i < n1;
         cs[i] = in ? A.w_scale[n0 + i] : 0.f;
-        cs[kN + i] = in && A.bias ? A.bias[n0 + i] : 0.f;
+        cs[kMaxN + i] = in && A.bias ? A.bias[n0 + i] : 0.f;
       }
       const long long m = (long long)tm * kRowsPerTile + (int)rank * kTileM + ew * 32 + lane;
       const float sx = m < A.M ? A.x_scale[m] : 0.f;
@@ -270,15 +296,14 @@ linear_i8_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_const
       if (!ok) continue;
       tc_fence_after();
 #pragma unroll 1
-      for (int c0 = 0; c0 < kN; c0 += kFlush < kN ? kFlush : kN) {
-        constexpr int kPart = (kFlush < kN ? kFlush : kN) / 32;
+      for (int c0 = 0; n0 + c0 < n1; c0 += kFlush) {   // a last part may reach beyond the tile: read, not stored
 #pragma unroll
-        for (int q = 0; q < kPart; ++q) {
+        for (int q = 0; q < kFlush / 32; ++q) {
           uint32_t r[32];
-          tmem_ld32(tmem + ((uint32_t)(ew * 32) << 16) + b * kN + c0 + 32 * q, r);
+          tmem_ld32(tmem + ((uint32_t)(ew * 32) << 16) + b * kMaxN + c0 + 32 * q, r);
           tmem_wait_ld_into(r);
           const float4* sw4 = reinterpret_cast<const float4*>(cs + c0 + 32 * q);
-          const float4* bi4 = reinterpret_cast<const float4*>(cs + kN + c0 + 32 * q);
+          const float4* bi4 = reinterpret_cast<const float4*>(cs + kMaxN + c0 + 32 * q);
           float v[32];
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
@@ -303,24 +328,39 @@ linear_i8_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_const
           }
         }
         __syncwarp();
-        // store: 8 lanes per row segment of 128 bytes, 4 rows at a time
-        const int c = n0 + c0 + (lane & 7) * kV;
-        const bool in_part = (lane & 7) * kV < kPart * 32;
-        const long long head = (long long)(c / A.d) * A.out_head + c % A.d;
+        if (p.vec) {
+          // 8 lanes per row segment of 128 bytes, 4 rows at a time
+          const int c = n0 + c0 + (lane & 7) * kV;
+          const long long head = (long long)(c / A.d) * A.out_head + c % A.d;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int row = i * 4 + (lane >> 3);
-          const long long ro = __shfl_sync(0xffffffffu, off, row);
-          const uint4 o = *reinterpret_cast<const uint4*>(stage + row * 128 + (((lane & 7) ^ (row & 7)) * 16));
-          if (row < valid && in_part && c < A.N) {
-            if (p.vec && c + kV <= A.N) {
-              *reinterpret_cast<uint4*>(static_cast<T*>(A.out) + ro + head) = o;
-            } else {
-              const T* e = reinterpret_cast<const T*>(&o);
+          for (int i = 0; i < 8; ++i) {
+            const int row = i * 4 + (lane >> 3);
+            const long long ro = __shfl_sync(0xffffffffu, off, row);
+            const uint4 o = *reinterpret_cast<const uint4*>(stage + row * 128 + (((lane & 7) ^ (row & 7)) * 16));
+            T* to = static_cast<T*>(A.out) + ro + head;
+            if (row < valid && c < n1) {
+              if (c + kV <= n1) {
+                *reinterpret_cast<uint4*>(to) = o;
+              } else {   // the last columns of the matrix: one head
+                const T* e = reinterpret_cast<const T*>(&o);
 #pragma unroll
-              for (int k = 0; k < kV; ++k)
-                if (c + k < A.N)
-                  static_cast<T*>(A.out)[ro + (long long)((c + k) / A.d) * A.out_head + (c + k) % A.d] = e[k];
+                for (int k = 0; k < kV; ++k)
+                  if (c + k < n1) to[k] = e[k];
+              }
+            }
+          }
+        } else {
+          // rows of any alignment: a row at a time, neighbouring lanes neighbouring columns
+#pragma unroll
+          for (int q = 0; q < kFlush / 32; ++q) {
+            const int col = 32 * q + lane, c = n0 + c0 + col;
+            const long long head = (long long)(c / A.d) * A.out_head + c % A.d;
+            const int byte = col * (int)sizeof(T);
+            for (int row = 0; row < valid; ++row) {
+              const long long ro = __shfl_sync(0xffffffffu, off, row);
+              if (c < n1)
+                static_cast<T*>(A.out)[ro + head] =
+                    *reinterpret_cast<const T*>(stage + row * 128 + (((byte >> 4) ^ (row & 7)) << 4) + (byte & 15));
             }
           }
         }
@@ -340,7 +380,7 @@ linear_i8_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_const
   if (kPair) cluster_sync();   // neither CTA's barriers or tensor memory go while the other may still reach them
   if (warp == 2) {
     tc_fence_after();
-    free_columns<kPair>(tmem, C::kColumns);
+    free_columns<kPair>(tmem, 2 * kMaxN);
   }
 }
 
@@ -356,28 +396,30 @@ bool make_tmap_i8(CUtensorMap* m, const void* ptr, uint64_t K, uint64_t rows, ui
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <typename T, bool kPair, int kN>
-cudaError_t launch_tile(const LinearArgs& a, int sms, int* status, cudaStream_t s) {
-  using C = Cfg<kPair, kN>;
-  static_assert(C::kSmem + 1024 <= 232448, "shared memory of one CTA per SM");
+template <typename T, bool kPair>
+cudaError_t launch_tile(const LinearArgs& a, int n, int sms, int* status, cudaStream_t s) {
   Params p;
   p.a = a;
   p.status = status;
+  p.n = n;
   p.tiles_m = (int)((a.M + (kPair ? 255 : 127)) / (kPair ? 256 : 128));
-  p.tiles_n = (a.N + kN - 1) / kN;
+  p.tiles_n = (a.N + n - 1) / n;
   p.k_blocks = (a.K + kBlockK - 1) / kBlockK;
-  // rows of x beyond a short matrix are not even zeroed: their products land in rows that are not stored
-  p.a_box_rows = a.M >= kTileM || kPair ? kTileM : ((int)a.M + 7) / 8 * 8;
+  p.a_rows = a.M >= kTileM || kPair ? kTileM : ((int)a.M + 7) / 8 * 8;
+  p.b_rows = kPair ? n / 2 : n;
+  const int slice = (p.a_rows + p.b_rows) * kBlockK;
+  p.sub = 32768 / slice < 1 ? 1 : 32768 / slice > 4 ? 4 : 32768 / slice;
+  p.stages = kRingBytes / (p.sub * slice) < kMaxStages ? kRingBytes / (p.sub * slice) : kMaxStages;
   const int esz = (int)sizeof(T), v = 16 / esz;
   p.vec = reinterpret_cast<uintptr_t>(a.out) % 16 == 0 && a.out_batch % v == 0 && a.out_token % v == 0 &&
           (a.d == a.N || (a.d % v == 0 && a.out_head % v == 0));
   // rows are at least their depth apart (the dispatch sees to it), one row may have any stride
   const uint64_t xs = a.M > 1 ? a.x_stride : (a.K + 15) / 16 * 16, ws = a.N > 1 ? a.w_stride : (a.K + 15) / 16 * 16;
   CUtensorMap tx, tw;
-  if (!make_tmap_i8(&tx, a.x, a.K, a.M, xs, p.a_box_rows)) return cudaErrorInvalidValue;
-  if (!make_tmap_i8(&tw, a.w, a.K, a.N, ws, C::kBRows)) return cudaErrorInvalidValue;
-  auto kernel = linear_i8_tc_kernel<T, kPair, kN>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem);
+  if (!make_tmap_i8(&tx, a.x, a.K, a.M, xs, p.a_rows)) return cudaErrorInvalidValue;
+  if (!make_tmap_i8(&tw, a.w, a.K, a.N, ws, p.b_rows)) return cudaErrorInvalidValue;
+  auto kernel = linear_i8_tc_kernel<T, kPair>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
   if (e != cudaSuccess) return e;
   const long long tiles = (long long)p.tiles_m * p.tiles_n;
   if (tiles >= (1LL << 30)) return cudaErrorInvalidValue;
@@ -385,7 +427,7 @@ cudaError_t launch_tile(const LinearArgs& a, int sms, int* status, cudaStream_t 
   const int slots = kPair ? sms / 2 : sms;
   cfg.gridDim = dim3((unsigned)(tiles < slots ? tiles : slots) * (kPair ? 2 : 1));
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = C::kSmem;
+  cfg.dynamicSmemBytes = kSmem;
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -396,17 +438,37 @@ cudaError_t launch_tile(const LinearArgs& a, int sms, int* status, cudaStream_t 
   return cudaLaunchKernelEx(&cfg, kernel, tx, tw, p);
 }
 
+// Columns of a single CTA's tile, or 0 for the pair, by an estimate of the clocks of the longest CTA: for each wave of tiles
+// and 32 of depth, the larger of the products (n / 2), their reads of shared memory (4 KB + 32 n bytes at 128 a clock)
+// and the loads of w at what one SM takes in (32 n bytes at 40 a clock; only few rows of x make this the larger), and
+// 2000 clocks a wave for filling the ring and the last epilogue.  The pair's tile takes 128 clocks; it reads
+// shared memory and L2 least, which the estimate of the single tile pays for with a quarter more.
+int choose_tile(const LinearArgs& a, int sms) {
+  const long long k = (a.K + 31) / 32;
+  long long best = (((a.M + 255) / 256) * ((a.N + 255) / 256) + sms / 2 - 1) / (sms / 2) * (128 * k + 2000);
+  int choice = 0;
+  const long long rows = (a.M + kTileM - 1) / kTileM;
+  for (int n = 16; n <= kMaxN; n += 16) {
+    const long long waves = (rows * ((a.N + n - 1) / n) + sms - 1) / sms;
+    const int mma = n / 2, smem = 32 + n / 4, load = a.M <= 32 ? n * 32 / 40 : 0;
+    const int step = mma > smem ? (mma > load ? mma : load) : (smem > load ? smem : load);
+    const long long clocks = waves * (step * k * 5 / 4 + 2000);
+    if (clocks < best || (clocks == best && choice)) {
+      best = clocks;
+      choice = n;
+    }
+  }
+  return choice;
+}
+
 template <typename T>
 cudaError_t launch_typed(const LinearArgs& a, int* status, cudaStream_t s) {
   int dev = 0, sms = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
-  const long long rows = (a.M + 127) / 128;
-  if (((a.M + 255) / 256) * ((a.N + 255) / 256) >= sms / 2) return launch_tile<T, true, 256>(a, sms, status, s);
-  if (rows * ((a.N + 127) / 128) >= sms) return launch_tile<T, false, 128>(a, sms, status, s);
-  if (rows * ((a.N + 63) / 64) >= sms) return launch_tile<T, false, 64>(a, sms, status, s);
-  return launch_tile<T, false, 32>(a, sms, status, s);
+  const int n = choose_tile(a, sms);
+  return n ? launch_tile<T, false>(a, n, sms, status, s) : launch_tile<T, true>(a, kMaxN, sms, status, s);
 }
 
 }  // namespace

@@ -491,8 +491,10 @@ da_status da_linear_i8(int B, int N, int H, int d, int K, const int8_t* x, int64
   const LinearArgs a{x, w, x_scale, w_scale, bias, out, M, (int)channels, K, d, N,
                      x_stride, w_stride, out_strides->batch, out_strides->head, out_strides->token};
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  return cuda_status(linear_i8_tc_supported(a) ? launch_linear_i8_tc(out_dtype == DA_BF16, a, static_cast<int*>(ws), s)
-                                               : launch_linear_i8_simt(out_dtype == DA_BF16, a, s));
+  const bool bf16 = out_dtype == DA_BF16;
+  if (!linear_i8_tc_supported(a)) return cuda_status(launch_linear_i8_simt(bf16, a, s));
+  if (linear_i8_rows_supported(a)) return cuda_status(launch_linear_i8_rows(bf16, a, s));
+  return cuda_status(launch_linear_i8_tc(bf16, a, static_cast<int*>(ws), s));
 }
 
 da_status da_rope(const da_rope_plan* plan, int B, int H, int N, int d, da_dtype dtype, const void* x,

@@ -93,6 +93,10 @@ struct LinearArgs {
 };
 cudaError_t launch_linear_i8_simt(bool bf16, const LinearArgs& a, cudaStream_t s);
 
+// linear_i8_rows.cu: few rows of x; needs linear_i8_tc_supported's alignment too
+bool linear_i8_rows_supported(const LinearArgs& a);
+cudaError_t launch_linear_i8_rows(bool bf16, const LinearArgs& a, cudaStream_t s);
+
 // linear_i8_tc.cu
 bool linear_i8_tc_supported(const LinearArgs& a);   // rows of x and w that TMA can read
 cudaError_t launch_linear_i8_tc(bool bf16, const LinearArgs& a, int* status, cudaStream_t s);

@@ -224,7 +224,7 @@ def _linear_close(got, x, sx, w, sw, bias, dtype):
 
 
 LINEAR = [(1, 1, 1), (1, 64, 16), (3, 17, 100), (16, 32, 128), (33, 257, 129), (64, 64, 1000), (127, 128, 256), (128, 129, 384),
-          (129, 255, 144), (200, 512, 640), (257, 640, 2048), (300, 96, 5120), (513, 1537, 1000), (1, 5120, 1536), (1000, 40, 64),
+          (129, 255, 144), (200, 512, 640), (257, 640, 2048), (300, 96, 5120), (513, 1537, 1000), (1, 5120, 1536), (2, 2500, 1555), (5, 601, 4111), (7, 2401, 2048), (8, 2, 15), (1000, 40, 64),
           (2, 30720, 256), (777, 3100, 72), (2049, 384, 128)]
 
 

@@ -418,6 +418,55 @@ def run_sip(args):
         "effective_flop_per_step": eff, "config": _config(w, args)}))
 
 
+def run_layer(args):
+    """One whole attention layer from hidden states (DecoupledLayer): residual addition and norm into
+    8-bit codes, 8-bit projections, query/key norm and rotary positions, reassign + attention, and the
+    8-bit output projection.  Milliseconds per step and of its two halves, by CUDA events."""
+    import block_sparse_cluster_b200 as da
+    w = W.WORKLOADS[args.workload]
+    if args.heads > 0:
+        w = W.scaled(w, H=args.heads)
+    dev = torch.device("cuda", 0)
+    dims = da.Dims(w.B, w.H, w.N, w.d, w.C, w.block, w.torch_dtype)
+    width = w.H * w.d
+    g = torch.Generator(device=dev).manual_seed(args.seed)
+
+    def normal(*shape, std=1.0, mean=0.0):
+        return torch.empty(*shape, dtype=w.torch_dtype, device=dev).normal_(mean, std, generator=g)
+    mats = [normal(width, width, std=width ** -0.5) for _ in range(4)]
+    norms = [normal(width, mean=1.0, std=0.1) for _ in range(3)]
+    weights = da.LayerWeights.quantize(norms[0], *mats, q_norm=norms[1], k_norm=norms[2])
+    half = w.d // 6 * 2
+    layer = da.DecoupledLayer(dims, width, weights, da.Rope(axes=(w.d - 2 * half, half, half), grid=(w.T, w.Hs, w.Ws)), device=dev)
+    plans = [[W.head_plan(w, args.seed, b, h) for h in range(w.H)] for b in range(w.B)]
+    kv_idx, kv_cnt = W.pack_plan(plans, w.nB)
+    layer.prepare(kv_idx.to(dev), kv_cnt.to(dev))
+    x, residual = normal(w.B, w.N, width), normal(w.B, w.N, width)
+    out = torch.empty_like(x)
+    layer.project(x, residual)
+    cent = layer.K[:, :, torch.randperm(w.N, generator=g, device=dev)[:w.C]].contiguous()
+    da.kmeans(dims, layer.K, cent, 3, layer.engine.stats, layer.engine.ws)
+    for _ in range(max(3, args.warmup)):
+        layer.step(x, cent, out)
+    ev = [[torch.cuda.Event(enable_timing=True) for _ in range(3)] for _ in range(args.steps)]
+    torch.cuda.synchronize(dev)
+    for e in ev:
+        e[0].record()
+        layer.project(x, residual)
+        e[1].record()
+        layer.attend(cent, out)
+        e[2].record()
+    torch.cuda.synchronize(dev)
+    if layer.status() != 0:
+        raise RuntimeError("device status after the timed steps")
+    part = lambda i, j: sum(e[i].elapsed_time(e[j]) for e in ev) / args.steps
+    print(json.dumps({
+        "metric": "ms/step of one 8-bit-projected decoupled attention layer", "value": part(0, 2), "unit": "ms",
+        "ms_per_step": part(0, 2), "breakdown_ms": {"project": part(0, 1), "attend": part(1, 2)}, "steps": args.steps,
+        "warmup": max(3, args.warmup), "higher_is_better": False, "dtype": w.dtype + " with int8 products",
+        "data": "synthetic", "products_flop": 8.0 * w.B * w.N * width * width, "config": _config(w, args)}))
+
+
 def main():
     ap = argparse.ArgumentParser()
     ap.add_argument("--gpus", type=int, default=1)
@@ -441,6 +490,8 @@ def main():
                     help="time the variance-corrected path (reassign + cluster spread + corrected attention)")
     ap.add_argument("--sip", action="store_true",
                     help="time the inclusion-probability reweighted attention (no compensation)")
+    ap.add_argument("--layer", action="store_true",
+                    help="time a whole attention layer from hidden states, with 8-bit projections")
     args = ap.parse_args()
     if args.loop:
         run_loop(args)
@@ -450,6 +501,9 @@ def main():
         return
     if args.sip:
         run_sip(args)
+        return
+    if args.layer:
+        run_layer(args)
         return
     ws, rank, local = _dist()
     w = W.WORKLOADS[args.workload]

@@ -559,3 +559,6 @@ class DecoupledAttention:
 
     def status(self, stream=None) -> int:
         return da_device_status(self.ws, stream)
+
+
+from .layer import DecoupledLayer, LayerWeights, quantize_weight  # noqa: E402  (uses the calls above)

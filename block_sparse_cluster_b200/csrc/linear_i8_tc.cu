@@ -4,14 +4,15 @@
 // tcgen05.mma kind::i8 sums in 32-bit integers in tensor memory, so the sum is exact; the epilogue
 // converts it, applies both scales and the bias in fp32 and rounds once to the output's type.
 //
-// A persistent grid walks output tiles.  Roles of a CTA (256 threads):
+// A persistent grid walks output tiles.  Roles of a CTA (384 threads):
 //   warp 0     lane 0 loads 128-byte slices of the x and w rows by TMA into a ring of stages (128-byte
 //              swizzle; rows and depth beyond the matrices read as zero);
 //   warp 1     lane 0 issues the products of a stage (four k = 32 steps) into one of two accumulators;
 //   warp 2     allocates tensor memory;
-//   warps 4-7  epilogue: accumulator -> scaled rows -> shared memory -> 16-byte stores of whole row segments
+//   warps 4-11 epilogue: accumulator -> scaled rows -> shared memory -> 16-byte stores of row segments
 //              (the matrix, or the attention's heads: the segment's address is formed from its token and
-//              head), while the next tile's products fill the other accumulator.
+//              head), while the next tile's products fill the other accumulator.  Two groups of four warps take
+//              alternate parts of 32 columns: one group alone was the bound at shallow depths.
 //
 // Two forms.  Pair (kPair): two CTAs of a cluster form a 256 x n tile (n 160 to 256) with cta_group::2; each loads its
 // own 128 rows of x and half of the w rows, so every loaded byte serves 256 rows or n columns.  Single: one CTA forms 128 x n,
@@ -30,14 +31,15 @@ namespace {
 
 constexpr int kBlockK = 128;                 // bytes (= elements) of depth per stage
 constexpr int kTileM = 128;                  // rows of x per CTA
-constexpr int kThreads = 256;
+constexpr int kEpilogueWarps = 8;
+constexpr int kThreads = 128 + 32 * kEpilogueWarps;
 constexpr int kABytes = kTileM * kBlockK;    // 16 KB
 constexpr int kGroupM = 8;                   // row tiles that are walked together for each column tile
 
 constexpr int kMaxN = 256;                   // columns of a tile
 constexpr int kMaxStages = 16;
 constexpr int kRingBytes = 6 * 32768;        // the pair's stages at n = 256; a single CTA's 128 + 256 rows fit four times
-constexpr int kStagingBytes = 4 * 4096;      // behind the ring, and at least the 16 KB that a short tile of x is read beyond it
+constexpr int kStagingBytes = kEpilogueWarps * 2048;   // 32 rows of 64 bytes a warp; behind the ring, and at least the 16 KB that a short tile of x is read beyond it
 constexpr size_t kSmem = 1024 + kRingBytes + kStagingBytes + 2 * 2 * kMaxN * 4 /*scales, bias*/;
 static_assert(kStagingBytes >= kABytes, "a short tile of x is read as a whole one");
 static_assert(kSmem + 1024 <= 232448, "shared memory of one CTA per SM");
@@ -175,7 +177,7 @@ __device__ __forceinline__ void tile_at(int t, const Params& p, int& tm, int& tn
   tm = g * kGroupM + r - tn * rows;
 }
 
-__device__ __forceinline__ void epilogue_barrier() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+__device__ __forceinline__ void epilogue_barrier() { asm volatile("bar.sync 1, %0;" ::"n"(32 * kEpilogueWarps) : "memory"); }
 
 template <typename T, bool kPair, int kSub>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -205,7 +207,7 @@ linear_i8_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_const
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&bars.acc_full[b], 1);
-      mbar_init(&bars.acc_empty[b], kPair ? 8 : 4);     // one arrival per epilogue warp
+      mbar_init(&bars.acc_empty[b], kPair ? 2 * kEpilogueWarps : kEpilogueWarps);   // one arrival per epilogue warp
     }
     mbar_init(&bars.drain, 1);
     bars.abort = 0;
@@ -300,103 +302,102 @@ linear_i8_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_const
       mbar_wait_drain(&bars.drain, 0);
     }
   } else if (warp >= 4) {
-    const int ew = warp & 3;
-    uint8_t* stage = staging + ew * 4096;
+    const int ew = warp & 3, half = (warp - 4) >> 2;   // rows ew * 32 .. + 32; parts half, half + 2, ...
+    uint8_t* stage = staging + (warp - 4) * 2048;
     const LinearArgs& A = p.a;
     constexpr int kV = 16 / (int)sizeof(T);          // elements of a 16-byte store
-    constexpr int kFlush = 128 / (int)sizeof(T);     // columns of a staged row
+    constexpr int kSeg = 64 / (int)sizeof(T);        // columns of a staged row
     const uint32_t empty0 = kPair ? map_to_rank(smem_u32(&bars.acc_empty[0]), 0) : 0;
     int n = 0;
-    bool ok = true;   // after a wait that gave up the loop still runs, so that the four warps' barriers match
+    bool ok = true;   // after a wait that gave up the loop still runs, so that the warps' barriers match
     for (int t = first; t < tiles; t += step, ++n) {
       int tm, tn;
       tile_at(t, p, tm, tn);
       const int b = n & 1;
       const int n0 = tn * p.n, n1 = min(n0 + p.n, A.N);   // the tile's columns
       float* cs = s_cols + b * 2 * kMaxN;
-      for (int i = threadIdx.x - 128; i < kMaxN; i += 128) {
+      for (int i = threadIdx.x - 128; i < kMaxN; i += 32 * kEpilogueWarps) {
         const bool in = n0 + i < n1;
         cs[i] = in ? A.w_scale[n0 + i] : 0.f;
         cs[kMaxN + i] = in && A.bias ? A.bias[n0 + i] : 0.f;
       }
       const long long m = (long long)tm * kRowsPerTile + (int)rank * kTileM + ew * 32 + lane;
       const float sx = m < A.M ? A.x_scale[m] : 0.f;
-      const long long off = (m / A.tokens) * A.out_batch + (m % A.tokens) * A.out_token;
+      const int mb = (int)m / A.tokens;   // M stays below 2^31
+      const long long off = mb * A.out_batch + ((int)m - mb * A.tokens) * A.out_token;
       const int valid = (int)min(32LL, max(0LL, A.M - (m - lane)));   // rows of this warp inside the matrix
       epilogue_barrier();
       ok = __all_sync(0xffffffffu, ok && mbar_wait(&bars.acc_full[b], (n >> 1) & 1, abort, p.status));
       if (!ok) continue;
       tc_fence_after();
 #pragma unroll 1
-      for (int c0 = 0; n0 + c0 < n1; c0 += kFlush) {   // a last part may reach beyond the tile: read, not stored
+      for (int c0 = 32 * half; n0 + c0 < n1; c0 += 64) {   // a last part may reach beyond the tile: read, not stored
+        uint32_t r[32];
+        tmem_ld32(tmem + ((uint32_t)(ew * 32) << 16) + b * kMaxN + c0, r);
+        tmem_wait_ld_into(r);
+        const float4* sw4 = reinterpret_cast<const float4*>(cs + c0);
+        const float4* bi4 = reinterpret_cast<const float4*>(cs + kMaxN + c0);
+        float v[32];
 #pragma unroll
-        for (int q = 0; q < kFlush / 32; ++q) {
-          uint32_t r[32];
-          tmem_ld32(tmem + ((uint32_t)(ew * 32) << 16) + b * kMaxN + c0 + 32 * q, r);
-          tmem_wait_ld_into(r);
-          const float4* sw4 = reinterpret_cast<const float4*>(cs + c0 + 32 * q);
-          const float4* bi4 = reinterpret_cast<const float4*>(cs + kMaxN + c0 + 32 * q);
-          float v[32];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const float4 w = sw4[i], bi = bi4[i];
-            v[4 * i] = fmaf((float)(int)r[4 * i] * sx, w.x, bi.x);
-            v[4 * i + 1] = fmaf((float)(int)r[4 * i + 1] * sx, w.y, bi.y);
-            v[4 * i + 2] = fmaf((float)(int)r[4 * i + 2] * sx, w.z, bi.z);
-            v[4 * i + 3] = fmaf((float)(int)r[4 * i + 3] * sx, w.w, bi.w);
-          }
-          // row `lane`, 16-byte chunk j at chunk j ^ (row & 7): neither side of the transposition conflicts
-#pragma unroll
-          for (int j = 0; j < 32 / kV; ++j) {
-            const int chunk = (q * 32 / kV + j) ^ (lane & 7);
-            uint4 o;
-            if (sizeof(T) == 2)
-              o = make_uint4(pack_bf16x2(v[8 * j], v[8 * j + 1]), pack_bf16x2(v[8 * j + 2], v[8 * j + 3]),
-                             pack_bf16x2(v[(8 * j + 4) % 32], v[(8 * j + 5) % 32]), pack_bf16x2(v[(8 * j + 6) % 32], v[(8 * j + 7) % 32]));
-            else
-              o = make_uint4(__float_as_uint(v[(4 * j) % 32]), __float_as_uint(v[(4 * j + 1) % 32]),
-                             __float_as_uint(v[(4 * j + 2) % 32]), __float_as_uint(v[(4 * j + 3) % 32]));
-            *reinterpret_cast<uint4*>(stage + lane * 128 + chunk * 16) = o;
-          }
+        for (int i = 0; i < 8; ++i) {
+          const float4 w = sw4[i], bi = bi4[i];
+          v[4 * i] = fmaf((float)(int)r[4 * i] * sx, w.x, bi.x);
+          v[4 * i + 1] = fmaf((float)(int)r[4 * i + 1] * sx, w.y, bi.y);
+          v[4 * i + 2] = fmaf((float)(int)r[4 * i + 2] * sx, w.z, bi.z);
+          v[4 * i + 3] = fmaf((float)(int)r[4 * i + 3] * sx, w.w, bi.w);
         }
-        __syncwarp();
-        if (p.vec) {
-          // 8 lanes per row segment of 128 bytes, 4 rows at a time
-          const int c = n0 + c0 + (lane & 7) * kV;
-          const long long head = (long long)(c / A.d) * A.out_head + c % A.d;
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int row = i * 4 + (lane >> 3);
-            const long long ro = __shfl_sync(0xffffffffu, off, row);
-            const uint4 o = *reinterpret_cast<const uint4*>(stage + row * 128 + (((lane & 7) ^ (row & 7)) * 16));
-            T* to = static_cast<T*>(A.out) + ro + head;
-            if (row < valid && c < n1) {
-              if (c + kV <= n1) {
-                *reinterpret_cast<uint4*>(to) = o;
-              } else {   // the last columns of the matrix: one head
-                const T* e = reinterpret_cast<const T*>(&o);
+        for (int g = 0; g < 32 / kSeg; ++g) {   // a segment of 64 bytes a row
+          // row `lane`, 16-byte chunk j at chunk j ^ (row / 2 & 3): neither side of the transposition conflicts
 #pragma unroll
-                for (int k = 0; k < kV; ++k)
-                  if (c + k < n1) to[k] = e[k];
+          for (int j = 0; j < 4; ++j) {
+            const float* e = v + g * kSeg + j * kV;
+            uint4 o;
+            if constexpr (sizeof(T) == 2)
+              o = make_uint4(pack_bf16x2(e[0], e[1]), pack_bf16x2(e[2], e[3]), pack_bf16x2(e[4], e[5]), pack_bf16x2(e[6], e[7]));
+            else
+              o = make_uint4(__float_as_uint(e[0]), __float_as_uint(e[1]), __float_as_uint(e[2]), __float_as_uint(e[3]));
+            *reinterpret_cast<uint4*>(stage + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4)) = o;
+          }
+          __syncwarp();
+          const int s0 = n0 + c0 + g * kSeg;   // the segment's first column
+          if (p.vec) {
+            // 4 lanes per row segment, 8 rows at a time
+            const int c = s0 + (lane & 3) * kV, h = c / A.d;
+            const long long head = h * A.out_head + (c - h * A.d);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int row = i * 8 + (lane >> 2);
+              const long long ro = __shfl_sync(0xffffffffu, off, row);
+              const uint4 o = *reinterpret_cast<const uint4*>(stage + row * 64 + (((lane & 3) ^ ((row >> 1) & 3)) << 4));
+              T* to = static_cast<T*>(A.out) + ro + head;
+              if (row < valid && c < n1) {
+                if (c + kV <= n1) {
+                  *reinterpret_cast<uint4*>(to) = o;
+                } else {   // the last columns of the matrix: one head
+                  const T* e = reinterpret_cast<const T*>(&o);
+#pragma unroll
+                  for (int k = 0; k < kV; ++k)
+                    if (c + k < n1) to[k] = e[k];
+                }
               }
             }
-          }
-        } else {
-          // rows of any alignment: a row at a time, neighbouring lanes neighbouring columns
-#pragma unroll
-          for (int q = 0; q < kFlush / 32; ++q) {
-            const int col = 32 * q + lane, c = n0 + c0 + col;
-            const long long head = (long long)(c / A.d) * A.out_head + c % A.d;
+          } else {
+            // rows of any alignment: kSeg lanes a row, neighbouring lanes neighbouring columns
+            constexpr int kRows = 32 / kSeg;
+            const int col = lane % kSeg, c = s0 + col, h = c / A.d;
+            const long long head = h * A.out_head + (c - h * A.d);
             const int byte = col * (int)sizeof(T);
-            for (int row = 0; row < valid; ++row) {
+            for (int i = 0; i < 32; i += kRows) {
+              const int row = i + lane / kSeg;
               const long long ro = __shfl_sync(0xffffffffu, off, row);
-              if (c < n1)
+              if (row < valid && c < n1)
                 static_cast<T*>(A.out)[ro + head] =
-                    *reinterpret_cast<const T*>(stage + row * 128 + (((byte >> 4) ^ (row & 7)) << 4) + (byte & 15));
+                    *reinterpret_cast<const T*>(stage + row * 64 + (((byte >> 4) ^ ((row >> 1) & 3)) << 4) + (byte & 15));
             }
           }
+          __syncwarp();
         }
-        __syncwarp();
       }
       tc_fence_before();
       __syncwarp();

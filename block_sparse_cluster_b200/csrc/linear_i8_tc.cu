@@ -87,8 +87,10 @@ __device__ __forceinline__ uint32_t map_to_rank(uint32_t addr, uint32_t rank) {
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
+// Arrive on a barrier of the other CTA (or this one).  What it orders is reads of tensor memory, which have completed and
+// been fenced (tcgen05.fence::before_thread_sync): a release at cluster scope would wait for the epilogue's global stores.
 __device__ __forceinline__ void arrive_at(uint32_t cluster_addr) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 
 // One lane of a converged warp.
@@ -310,19 +312,36 @@ linear_i8_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_const
     const uint32_t empty0 = kPair ? map_to_rank(smem_u32(&bars.acc_empty[0]), 0) : 0;
     int n = 0;
     bool ok = true;   // after a wait that gave up the loop still runs, so that the warps' barriers match
+    // scales and bias of a tile: thread i of the epilogue holds column i's, and its row's scale; loaded a tile ahead
+    static_assert(32 * kEpilogueWarps == kMaxN, "a thread a column");
+    const int mine = threadIdx.x - 128;
+    float col_scale = 0.f, col_bias = 0.f, row_scale = 0.f;
+    auto load_scales = [&](int t) {
+      int tm, tn;
+      tile_at(t, p, tm, tn);
+      const int c = tn * p.n + mine;
+      const long long m = (long long)tm * kRowsPerTile + (int)rank * kTileM + ew * 32 + lane;
+      col_scale = col_bias = row_scale = 0.f;
+      if (t < tiles) {
+        if (mine < p.n && c < A.N) {
+          col_scale = A.w_scale[c];
+          if (A.bias) col_bias = A.bias[c];
+        }
+        if (m < A.M) row_scale = A.x_scale[m];
+      }
+    };
+    load_scales(first);
     for (int t = first; t < tiles; t += step, ++n) {
       int tm, tn;
       tile_at(t, p, tm, tn);
       const int b = n & 1;
       const int n0 = tn * p.n, n1 = min(n0 + p.n, A.N);   // the tile's columns
       float* cs = s_cols + b * 2 * kMaxN;
-      for (int i = threadIdx.x - 128; i < kMaxN; i += 32 * kEpilogueWarps) {
-        const bool in = n0 + i < n1;
-        cs[i] = in ? A.w_scale[n0 + i] : 0.f;
-        cs[kMaxN + i] = in && A.bias ? A.bias[n0 + i] : 0.f;
-      }
+      cs[mine] = col_scale;
+      cs[kMaxN + mine] = col_bias;
+      const float sx = row_scale;
+      load_scales(t + step);
       const long long m = (long long)tm * kRowsPerTile + (int)rank * kTileM + ew * 32 + lane;
-      const float sx = m < A.M ? A.x_scale[m] : 0.f;
       const int mb = (int)m / A.tokens;   // M stays below 2^31
       const long long off = mb * A.out_batch + ((int)m - mb * A.tokens) * A.out_token;
       const int valid = (int)min(32LL, max(0LL, A.M - (m - lane)));   // rows of this warp inside the matrix
@@ -335,16 +354,17 @@ linear_i8_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_const
         uint32_t r[32];
         tmem_ld32(tmem + ((uint32_t)(ew * 32) << 16) + b * kMaxN + c0, r);
         tmem_wait_ld_into(r);
-        const float4* sw4 = reinterpret_cast<const float4*>(cs + c0);
-        const float4* bi4 = reinterpret_cast<const float4*>(cs + kMaxN + c0);
+        const ulonglong2* sw2 = reinterpret_cast<const ulonglong2*>(cs + c0);
+        const ulonglong2* bi2 = reinterpret_cast<const ulonglong2*>(cs + kMaxN + c0);
+        const uint64_t sx2 = f2_pack(sx, sx);
         float v[32];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const float4 w = sw4[i], bi = bi4[i];
-          v[4 * i] = fmaf((float)(int)r[4 * i] * sx, w.x, bi.x);
-          v[4 * i + 1] = fmaf((float)(int)r[4 * i + 1] * sx, w.y, bi.y);
-          v[4 * i + 2] = fmaf((float)(int)r[4 * i + 2] * sx, w.z, bi.z);
-          v[4 * i + 3] = fmaf((float)(int)r[4 * i + 3] * sx, w.w, bi.w);
+          const ulonglong2 w = sw2[i], bi = bi2[i];
+          const uint64_t lo = f2_pack((float)(int)r[4 * i], (float)(int)r[4 * i + 1]);
+          const uint64_t hi = f2_pack((float)(int)r[4 * i + 2], (float)(int)r[4 * i + 3]);
+          f2_unpack(f2_fma(f2_mul(lo, sx2), w.x, bi.x), v[4 * i], v[4 * i + 1]);
+          f2_unpack(f2_fma(f2_mul(hi, sx2), w.y, bi.y), v[4 * i + 2], v[4 * i + 3]);
         }
 #pragma unroll
         for (int g = 0; g < 32 / kSeg; ++g) {   // a segment of 64 bytes a row

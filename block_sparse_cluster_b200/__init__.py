@@ -388,8 +388,9 @@ def _head_strides(t: torch.Tensor, where: str, what: str) -> _HeadStrides:
 
 def _on(device: int, stream, f, *args) -> int:
     """f(*args, stream) with `device` current; the stream is the device's current one by default."""
+    # the raw calls cost a tenth of torch.cuda's, which matters for the smallest operators
     raw = torch._C._cuda_getCurrentRawStream(device) if stream is None else _stream(stream)
-    if device == torch.cuda.current_device():
+    if device == torch._C._cuda_getDevice():
         return f(*args, raw)
     with torch.cuda.device(device):
         return f(*args, raw)
@@ -483,6 +484,7 @@ def da_linear_i8(x: torch.Tensor, x_scale: torch.Tensor, w: torch.Tensor, w_scal
     return out
 
 
+_I3 = _I * 3
 PAIRINGS = {"adjacent": 0, "halves": 1}
 
 
@@ -498,7 +500,7 @@ class Rope:
     def c(self) -> _RopePlan:
         if len(self.axes) != 3 or len(self.grid) != 3 or self.pairing not in PAIRINGS:
             raise DAError(_INVALID_ARG, "Rope: three axes, a grid of three and a pairing of " + " or ".join(PAIRINGS))
-        return _RopePlan((_I * 3)(*self.axes), (_I * 3)(*self.grid), self.theta, PAIRINGS[self.pairing])
+        return _RopePlan(_I3(*self.axes), _I3(*self.grid), self.theta, PAIRINGS[self.pairing])
 
 
 def da_rope(x: torch.Tensor, out: torch.Tensor, rope: Rope, positions: Optional[torch.Tensor] = None,

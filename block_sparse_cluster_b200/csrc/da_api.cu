@@ -508,7 +508,7 @@ da_status da_rope(const da_rope_plan* plan, int B, int H, int N, int d, da_dtype
   if (st != DA_OK) return st;
   if (d != 64 && d != 128) return DA_ERR_UNSUPPORTED;
   if (plan->pairing != DA_ROPE_ADJACENT && plan->pairing != DA_ROPE_HALVES) return DA_ERR_INVALID_ARG;
-  if (!(plan->theta > 0.0) || !(plan->theta < 1e30)) return DA_ERR_INVALID_ARG;
+  if (!(plan->theta >= 1.0) || !(plan->theta < 1e30)) return DA_ERR_INVALID_ARG;
   long long dims = 0, cells = 1;
   for (int u = 0; u < 3; ++u) {
     if (plan->axis_dims[u] < 0 || plan->axis_dims[u] % 2 != 0) return DA_ERR_SHAPE;

@@ -5,8 +5,9 @@
 // index within the axis:  (a, b) -> (a cos - b sin, a sin + b cos).
 // Positions come from the (time, height, width) grid of the token's index, or from the caller.
 //
-// Angles are formed in fp64 in units of half turns, reduced to [-1, 1] there, and only then
-// rounded for sincospif: position times frequency loses nothing however far the position.
+// Angles are formed in whole turns of 2^64: a frequency is a 64-bit fraction of a turn per position, and position times
+// frequency modulo 2^64 is what is left of the angle after its whole turns, exactly, however far the position and whatever
+// its sign.  Only the upper 32 bits, as half turns in [-1, 1), are rounded to fp32 for sincospif.
 //
 // The kernel is bound by HBM: x is read once and out written once.  A thread's unit of work is two
 // 16-byte vectors of a head, elements [j, j + V) and [j + d/2, j + d/2 + V): whole pairs in either pairing.
@@ -43,7 +44,7 @@ struct RopeArgs {
   int grid[3];
   int norm, halves;
   float eps, inv_width;        // 1 / (H d)
-  double freq[kMaxPairs];      // frequency / pi: half turns per position
+  uint64_t freq[kMaxPairs];    // 2^-64 turns per position
   unsigned char axis[kMaxPairs];
 };
 
@@ -151,7 +152,7 @@ __global__ void __launch_bounds__(512, UPT == 1 ? 2 : 1) rope_kernel(const __gri
   float* const s_cos = reinterpret_cast<float*>(s_ring + kStages * UPT * 2 * blockDim.x);   // [token of the run][pair]
   float* const s_sin = s_cos + a.run * (D / 2);
   __shared__ int4 s_pos[kMaxRun];   // time, height, width, whether the token turns at all
-  __shared__ double s_freq[D / 2];
+  __shared__ uint64_t s_freq[D / 2];
   __shared__ unsigned char s_axis[D / 2];
   __shared__ float s_part[2][16];
   const int b = blockIdx.y, n0 = blockIdx.x * a.run, h0 = blockIdx.z * a.heads_per_block;
@@ -217,9 +218,8 @@ __global__ void __launch_bounds__(512, UPT == 1 ? 2 : 1) rope_kernel(const __gri
   for (int i = threadIdx.x; i < run * (D / 2); i += blockDim.x) {
     const int p = i % (D / 2);
     const int pos = reinterpret_cast<const int*>(&s_pos[i / (D / 2)])[s_axis[p]];
-    double half_turns = (double)pos * s_freq[p];
-    half_turns -= 2.0 * rint(half_turns * 0.5);
-    sincospif((float)half_turns, &s_sin[i], &s_cos[i]);
+    const int turn = (int)(((uint64_t)(int64_t)pos * s_freq[p]) >> 32);   // 2^-31 half turns
+    sincospif((float)turn * 0x1p-31f, &s_sin[i], &s_cos[i]);
   }
   __syncthreads();
 
@@ -377,12 +377,18 @@ cudaError_t launch_rope(bool bf16, const da_rope_plan& plan, int B, int H, int N
   a.eps = eps;
   a.inv_width = 1.f / ((float)H * (float)d);
   a.halves = plan.pairing == DA_ROPE_HALVES;
+  // theta^(-2j / D) / (2 pi) turns, in the 64-bit mantissa of long double; theta >= 1 keeps it below one
   int p = 0;
-  for (int u = 0; u < 3; ++u)
-    for (int j = 0; j < plan.axis_dims[u] / 2; ++j, ++p) {
-      a.freq[p] = pow(plan.theta, -2.0 * j / plan.axis_dims[u]) / M_PI;
+  for (int u = 0; u < 3; ++u) {
+    const int D = plan.axis_dims[u];
+    if (D == 0) continue;
+    const long double ratio = powl((long double)plan.theta, -2.0L / D);
+    long double f = 0.159154943091895335768883763372514362L;
+    for (int j = 0; j < D / 2; ++j, ++p, f *= ratio) {
+      a.freq[p] = (uint64_t)ldexpl(f, 64);
       a.axis[p] = (unsigned char)u;
     }
+  }
   if (bf16) return d == 128 ? launch_typed<__nv_bfloat16, 128>(a, B, s) : launch_typed<__nv_bfloat16, 64>(a, B, s);
   return d == 128 ? launch_typed<float, 128>(a, B, s) : launch_typed<float, 64>(a, B, s);
 }

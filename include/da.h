@@ -384,7 +384,7 @@ typedef struct {
   int axis_dims[3];   /* elements of a head that each axis turns: even, sum d; an axis may have none */
   int grid[3];        /* token n of the grid has position (n / (grid[1] grid[2]), n / grid[2] % grid[1], n % grid[2]);
                          used, and positive, where no positions are given */
-  double theta;       /* frequency j of an axis of D elements is theta^(-2j / D); 0 < theta < 1e30 */
+  double theta;       /* frequency j of an axis of D elements is theta^(-2j / D); 1 <= theta < 1e30 */
   int pairing;        /* a da_rope_pairing */
 } da_rope_plan;
 
@@ -399,7 +399,7 @@ typedef struct {
  * the grid (text behind a video) are not turned: they are copied, or normed only.
  * weight: NULL, or the norm's weight of dtype, with x first replaced by x / sqrt(mean(x^2) + eps) *
  * weight: the mean over the head's d elements if weight_width = d, over all of a token's heads if
- * weight_width = H * d (<= 16384).  Angles are formed in fp64; norm and rotation in fp32, rounded once.
+ * weight_width = H * d (<= 16384).  Angles lose no whole turn at any position; norm and rotation are in fp32, rounded once.
  * out may be x.
  */
 DA_API da_status da_rope(const da_rope_plan* plan, int B, int H, int N, int d, da_dtype dtype, const void* x,

@@ -12,7 +12,7 @@ Tolerances, with u = 2^-24 (half a step of fp32) and h(t) = finfo(t).eps / 2 (ha
   3u of |p| (p the scaled sum without bias) and the output's rounding h.
 * rotation: the angle in half turns is at most 1 and rounds to fp32 with 2^-25, pi 2^-25 = 1.6u in the angle; sin and cos
   are within 1 ulp (2u at most); products and sum round once each.  7u (|a| + |b|), after a norm 23u more: 2^-18 = 64u of
-  |a| + |b| is allowed, plus h.  Positions stay below 2^24, where fp64 angles lose less than 2^-25.
+  |a| + |b| is allowed, plus h.  Positions stay below 2^24, where the oracle's fp64 angles lose less than 2^-25.
 """
 import numpy as np
 import pytest

@@ -94,7 +94,7 @@ def _rope(plan=True, axes=(24, 20, 20), grid=(2, 2, 4), theta=1e4, pairing=0, B=
     (dict(plan=False), INVALID), (dict(B=0), INVALID), (dict(H=0), INVALID), (dict(N=0), INVALID), (dict(d=0), INVALID),
     (dict(x=None), INVALID), (dict(xs=None), INVALID), (dict(o=None), INVALID), (dict(os_=None), INVALID),
     (dict(dtype=2), DTYPE), (dict(d=96, axes=(32, 32, 32)), UNSUPPORTED), (dict(pairing=2), INVALID), (dict(pairing=-1), INVALID),
-    (dict(theta=0.0), INVALID), (dict(theta=-1.0), INVALID), (dict(theta=float("nan")), INVALID),
+    (dict(theta=0.0), INVALID), (dict(theta=-1.0), INVALID), (dict(theta=0.5), INVALID), (dict(theta=float("nan")), INVALID),
     (dict(theta=float("inf")), INVALID),
     (dict(axes=(24, 21, 19)), SHAPE), (dict(axes=(24, 20, 18)), SHAPE), (dict(axes=(-2, 46, 20)), SHAPE),
     (dict(grid=(0, 2, 4)), SHAPE), (dict(grid=(1 << 16, 1 << 15, 1)), SHAPE), (dict(B=1 << 16, N=1 << 16), SHAPE),

@@ -88,6 +88,14 @@ da_status check_mask(const Dims& g, const da_block_mask* mask) {
 
 da_status cuda_status(cudaError_t e) { return e == cudaSuccess ? DA_OK : DA_ERR_CUDA; }
 
+// Rows, tokens and the like stay this far below 2^31, so that a grid's last blocks index beyond them in 32 bits.
+constexpr long long kMaxTokens = (1LL << 31) - 65536;
+
+// Strides of dimensions of one entry are never used: zero, so that no check takes offence at them.
+da_head_strides used_strides(int B, int H, int N, const da_head_strides& s) {
+  return da_head_strides{B > 1 ? s.batch : 0, H > 1 ? s.head : 0, N > 1 ? s.token : 0};
+}
+
 // A strided tensor of the layer operators: up to three outer dimensions over `inner` contiguous
 // elements of `size` bytes.
 struct View {
@@ -96,15 +104,18 @@ struct View {
   int size;
   long long n[3], stride[3];
 
-  bool fits() const {   // strides and extents whose byte offsets stay far inside 64 bits
-    for (int i = 0; i < 3; ++i)
-      if (stride[i] < 0 || stride[i] > (1LL << 40) || n[i] >= (1LL << 31)) return false;
-    return span() < (1LL << 46);
+  bool fits() const {   // strides and extents whose offsets stay far inside 64 bits
+    __int128 s = inner;
+    for (int i = 0; i < 3; ++i) {
+      if (stride[i] < 0 || stride[i] > (1LL << 40) || n[i] > kMaxTokens) return false;
+      if (n[i] > 1) s += (__int128)(n[i] - 1) * stride[i];
+    }
+    return s < (__int128)1 << 46;
   }
-  long long span() const {   // elements from the first to the last, both included
+  long long span() const {   // elements from the first to the last, both included; of a view that fits
     long long s = inner;
     for (int i = 0; i < 3; ++i)
-      if (n[i] > 1) s += (n[i] - 1) * stride[i] < 0 ? (1LL << 46) : (n[i] - 1) * stride[i];
+      if (n[i] > 1) s += (n[i] - 1) * stride[i];
     return s;
   }
   // No element twice: each outer dimension, from the smallest stride up, steps over what lies below it.
@@ -456,12 +467,13 @@ da_status da_quantize_i8(int B, int H, int N, int d, da_dtype dtype, const void*
   if (st != DA_OK) return st;
   if ((long long)H * d > kMaxRowWidth) return DA_ERR_UNSUPPORTED;
   const long long rows = (long long)B * N;
-  const View vx = heads(x, element_size(dtype), B, H, N, d, *x_strides);
+  const da_head_strides xs = used_strides(B, H, N, *x_strides);
+  const View vx = heads(x, element_size(dtype), B, H, N, d, xs);
   const View vq = matrix(q, 1, rows, H * d, q_stride), vc = matrix(scale, 4, rows, 1, 1);
-  if (B > 65535 || rows >= (1LL << 31) || !vx.fits() || !vq.fits() || !vq.distinct()) return DA_ERR_SHAPE;
+  if (B > 65535 || rows > kMaxTokens || !vx.fits() || !vq.fits() || !vq.distinct()) return DA_ERR_SHAPE;
   if (!vx.element_aligned() || !vc.element_aligned()) return DA_ERR_ALIGNMENT;
   if (!apart(vq, vx, false) || !apart(vq, vc, false) || !apart(vc, vx, false)) return DA_ERR_INVALID_ARG;
-  return cuda_status(launch_quantize_i8(dtype == DA_BF16, B, H, N, d, x, *x_strides, q, q_stride, scale,
+  return cuda_status(launch_quantize_i8(dtype == DA_BF16, B, H, N, d, x, xs, q, q_stride, scale,
                                         reinterpret_cast<cudaStream_t>(stream)));
 }
 
@@ -476,11 +488,12 @@ da_status da_linear_i8(int B, int N, int H, int d, int K, const int8_t* x, int64
   // 128 * 128 * K has to stay below 2^31
   if (K > 131071) return DA_ERR_UNSUPPORTED;
   const long long M = (long long)B * N, channels = (long long)H * d;
-  if (M >= (1LL << 31) || channels > (1 << 22) - 64) return DA_ERR_SHAPE;
+  if (M > kMaxTokens || channels > (1 << 22) - 64) return DA_ERR_SHAPE;
   const View vx = matrix(x, 1, M, K, x_stride), vw = matrix(w, 1, channels, K, w_stride);
   const View vsx = matrix(x_scale, 4, M, 1, 1), vsw = matrix(w_scale, 4, channels, 1, 1);
   const View vb = matrix(bias, 4, channels, 1, 1);
-  const View vo = heads(out, element_size(out_dtype), B, H, N, d, *out_strides);
+  const da_head_strides os = used_strides(B, H, N, *out_strides);
+  const View vo = heads(out, element_size(out_dtype), B, H, N, d, os);
   if (!vx.fits() || !vw.fits() || !vo.fits() || !vo.distinct()) return DA_ERR_SHAPE;
   if (!vsx.element_aligned() || !vsw.element_aligned() || !vb.element_aligned() || !vo.element_aligned() || !aligned16(ws))
     return DA_ERR_ALIGNMENT;
@@ -489,7 +502,7 @@ da_status da_linear_i8(int B, int N, int H, int d, int K, const int8_t* x, int64
       !apart(vo, vb, false) || !apart(vo, matrix(ws, 1, 1, kStatusWords * sizeof(int), 0), false))
     return DA_ERR_INVALID_ARG;
   const LinearArgs a{x, w, x_scale, w_scale, bias, out, M, (int)channels, K, d, N,
-                     x_stride, w_stride, out_strides->batch, out_strides->head, out_strides->token};
+                     x_stride, w_stride, os.batch, os.head, os.token};
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const bool bf16 = out_dtype == DA_BF16;
   if (!linear_i8_tc_supported(a)) return cuda_status(launch_linear_i8_simt(bf16, a, s));
@@ -523,17 +536,18 @@ da_status da_rope(const da_rope_plan* plan, int B, int H, int N, int d, da_dtype
     return weight_width != d && weight_width != (long long)H * d ? DA_ERR_SHAPE : DA_ERR_INVALID_ARG;
   if (weight && weight_width != d && weight_width > kMaxRowWidth) return DA_ERR_UNSUPPORTED;
   const int size = element_size(dtype);
-  const View vx = heads(x, size, B, H, N, d, *x_strides), vo = heads(out, size, B, H, N, d, *out_strides);
+  const da_head_strides xs = used_strides(B, H, N, *x_strides), os = used_strides(B, H, N, *out_strides);
+  const View vx = heads(x, size, B, H, N, d, xs), vo = heads(out, size, B, H, N, d, os);
   const View vw = matrix(weight, size, 1, weight ? weight_width : 1, 0);
   const View vp = View{positions, 3, 4, {1, B, N}, {0, positions_batch, 3}};
-  if (B > 65535 || H > 65535 || (long long)B * N >= (1LL << 31)) return DA_ERR_SHAPE;
+  if (B > 65535 || H > 65535 || (long long)B * N > kMaxTokens) return DA_ERR_SHAPE;
   if (!vx.fits() || !vo.fits() || !vo.distinct()) return DA_ERR_SHAPE;
   if (positions && (!vp.fits() || (positions_batch != 0 && positions_batch < 3LL * N))) return DA_ERR_SHAPE;
   if (!vx.aligned16() || !vo.aligned16() || reinterpret_cast<uintptr_t>(weight) % 16 != 0 || !vp.element_aligned())
     return DA_ERR_ALIGNMENT;
   if (!apart(vo, vx, true) || !apart(vo, vw, false) || !apart(vo, vp, false)) return DA_ERR_INVALID_ARG;
-  return cuda_status(launch_rope(dtype == DA_BF16, *plan, B, H, N, d, x, *x_strides, positions, positions_batch, weight,
-                                 weight_width, eps, out, *out_strides, reinterpret_cast<cudaStream_t>(stream)));
+  return cuda_status(launch_rope(dtype == DA_BF16, *plan, B, H, N, d, x, xs, positions, positions_batch, weight,
+                                 weight_width, eps, out, os, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 da_status da_device_status(void* ws, da_stream stream) {

@@ -317,18 +317,15 @@ linear_i8_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_const
     const int mine = threadIdx.x - 128;
     float col_scale = 0.f, col_bias = 0.f, row_scale = 0.f;
     auto load_scales = [&](int t) {
+      if (t >= tiles) return;
       int tm, tn;
       tile_at(t, p, tm, tn);
       const int c = tn * p.n + mine;
       const long long m = (long long)tm * kRowsPerTile + (int)rank * kTileM + ew * 32 + lane;
-      col_scale = col_bias = row_scale = 0.f;
-      if (t < tiles) {
-        if (mine < p.n && c < A.N) {
-          col_scale = A.w_scale[c];
-          if (A.bias) col_bias = A.bias[c];
-        }
-        if (m < A.M) row_scale = A.x_scale[m];
-      }
+      const bool in = mine < p.n && c < A.N;
+      col_scale = in ? A.w_scale[c] : 0.f;
+      col_bias = in && A.bias ? A.bias[c] : 0.f;
+      row_scale = m < A.M ? A.x_scale[m] : 0.f;
     };
     load_scales(first);
     for (int t = first; t < tiles; t += step, ++n) {
@@ -555,8 +552,7 @@ bool linear_i8_tc_supported(const LinearArgs& a) {
   auto rows_ok = [&](const void* p, long long rows, long long stride) {
     return reinterpret_cast<uintptr_t>(p) % 16 == 0 && (rows == 1 || (stride % 16 == 0 && stride >= a.K && stride < (1LL << 40)));
   };
-  // tile rows are 32-bit coordinates
-  return a.M < (1LL << 31) - 256 && rows_ok(a.x, a.M, a.x_stride) && rows_ok(a.w, a.N, a.w_stride);
+  return rows_ok(a.x, a.M, a.x_stride) && rows_ok(a.w, a.N, a.w_stride);
 }
 
 cudaError_t launch_linear_i8_tc(bool bf16, const LinearArgs& a, int* status, cudaStream_t s) {

@@ -298,8 +298,9 @@ DA_API da_status da_noalloc_device_status(da_stream stream);
  *   K, rotary positions, heads) -> da_reassign + da_attention -> da_quantize_i8 -> da_linear_i8
  *
  * Conventions beside the shared ones above: every tensor has strides, in elements, and its
- * innermost dimension is contiguous.  Sizes are positive (DA_ERR_INVALID_ARG otherwise); a row or
- * token index stays below 2^31 and every stride below 2^40 (DA_ERR_SHAPE otherwise).  Inputs may
+ * innermost dimension is contiguous.  Sizes are positive (DA_ERR_INVALID_ARG otherwise); rows, and
+ * tokens over the batch, number at most 2^31 - 65536, no stride exceeds 2^40 and no tensor spans more than
+ * 2^46 elements (DA_ERR_SHAPE otherwise).  Inputs may
  * repeat rows (stride 0); an output whose strides make two of its elements share memory is
  * DA_ERR_SHAPE.  An output may share memory with an input only where a call says so, and then
  * both are the same elements (base and strides); any other overlap of the address ranges is
@@ -322,7 +323,8 @@ typedef struct {
  * the products are held in fp32 (v is not rounded to dtype before the norm); out and sum_out are rounded
  * once.  out may be x or residual, sum_out may be x or residual (the residual stream updated in
  * place), but not the same buffer.  width <= 16384 (DA_ERR_UNSUPPORTED above); eps >= 0.  A row with an infinity
- * or NaN gives what the formula gives; so does one whose squares leave fp32's range (|v| above about 1e19).
+ * or NaN gives what the formula gives in fp32; so does one whose sum of squares leaves fp32's range (|v| above about 1e18, or,
+ * with eps = 0, below about 1e-22).
  */
 DA_API da_status da_rms_norm(int64_t rows, int width, da_dtype dtype, const void* x, int64_t x_stride,
                              const void* residual, int64_t residual_stride, const void* weight, float eps,

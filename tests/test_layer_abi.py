@@ -26,7 +26,8 @@ def _norm_i8(rows=10, width=64, dtype=0, x=X, xs=64, r=R, rs=64, w=W, eps=1e-6, 
     (dict(o=None), INVALID), (dict(r=None), INVALID),            # a sum without a residual
     (dict(eps=-1.0), INVALID), (dict(eps=float("nan")), INVALID), (dict(eps=float("inf")), INVALID),
     (dict(dtype=2), DTYPE), (dict(dtype=-1), DTYPE), (dict(width=16385, xs=16385, rs=16385, ss=16385, os_=16385), UNSUPPORTED),
-    (dict(rows=1 << 31), SHAPE), (dict(xs=-64), SHAPE), (dict(xs=1 << 41), SHAPE), (dict(os_=63), SHAPE),
+    (dict(rows=1 << 31), SHAPE), (dict(rows=(1 << 31) - 65535), SHAPE), (dict(rows=(1 << 31) - 65536, os_=1 << 40), SHAPE),
+    (dict(rows=(1 << 24) + 1, xs=1 << 40), SHAPE), (dict(xs=-64), SHAPE), (dict(xs=1 << 41), SHAPE), (dict(os_=63), SHAPE),
     (dict(os_=0), SHAPE), (dict(ss=63), SHAPE),
     (dict(x=X + 1), ALIGN), (dict(r=R + 1), ALIGN), (dict(w=W + 1), ALIGN), (dict(s=S + 1), ALIGN),
     (dict(s=O), INVALID), (dict(o=W), INVALID), (dict(s=W), INVALID), (dict(s=X + 2), INVALID), (dict(s=R + 128), INVALID),

@@ -190,6 +190,86 @@ def test_codes_next_to_borders(width):
     assert np.array_equal(q.cpu().numpy().astype(np.int64), rq)
 
 
+def test_codes_of_every_bf16_quotient():
+    """Every 8-bit t against every 8-bit maximum, twelve binades down, both signs: all ties of the bf16 quantiser."""
+    T = torch.arange(128, 256).double()
+    t = torch.cat([T * 2.0 ** -s for s in range(12)])
+    rows = []
+    for M in range(128, 256):
+        r = t.clone()
+        r[r > M] = 0
+        rows.append(torch.cat([r, -r, torch.tensor([float(M)] * 8).double()]))
+    x = torch.stack(rows).to(BF16)
+    for width in (x.shape[1], x.shape[1] - 3):              # by vectors and one by one
+        part = x[:, -width:].contiguous()
+        q, scale = torch.empty(128, width, dtype=torch.int8, device="cuda"), torch.empty(128, device="cuda")
+        da.da_quantize_i8(part.cuda(), q, scale)
+        ref, m = oracle.row_codes(part)
+        assert np.array_equal(q.cpu().numpy().astype(np.int64), ref)
+        # the same rows as a norm's input, whose second looks settle them
+        da.da_rms_norm_i8(part.cuda(), None, q, scale)
+        assert np.array_equal(q.cpu().numpy().astype(np.int64), ref)
+
+
+@pytest.mark.parametrize("width", [1536, 3000, 777])
+def test_codes_of_many_rows(width):
+    """Thousands of rows, so that maxima that meet, ties at half the maximum and second looks all turn up."""
+    g = _gen(width)
+    x = torch.randn(3000, width, generator=g).to(BF16)
+    r = torch.randn(3000, width, generator=g).to(BF16)
+    w = (1 + 0.1 * torch.randn(width, generator=g)).to(BF16)
+    q, scale = torch.empty(3000, width, dtype=torch.int8, device="cuda"), torch.empty(3000, device="cuda")
+    for residual, weight in ((None, None), (r, w), (x, None)):   # the last: the residual is x itself
+        xc = x.cuda()
+        rc = xc if residual is x else _cuda(residual)
+        da.da_rms_norm_i8(xc, _cuda(weight), q, scale, residual=rc)
+        ref, _, _ = oracle.rms_norm_i8(x, residual, weight)
+        assert np.array_equal(q.cpu().numpy().astype(np.int64), ref)
+
+
+def test_rows_and_heads_at_a_distance():
+    """Strides whose offsets pass 32 bits, in elements and in bytes."""
+    big = torch.empty(3 * (1 << 31) + 4096, dtype=BF16, device="cuda")
+    step = (1 << 31) + 64
+    g = _gen(4)
+    x = big.as_strided((3, 512), (step, 1))
+    x.copy_(torch.randn(3, 512, generator=g).to(BF16))
+    q, scale, out = torch.empty(3, 512, dtype=torch.int8, device="cuda"), torch.empty(3, device="cuda"), torch.empty(3, 512, dtype=BF16, device="cuda")
+    da.da_rms_norm(x, None, out)
+    _norm_close(out, oracle.rms_norm(x.cpu())[0], BF16)
+    da.da_rms_norm(out, None, x)                                 # and into far rows
+    _norm_close(x, oracle.rms_norm(out.cpu())[0], BF16)
+    for strides in ((0, step, 128, 1), (0, 128, step, 1)):           # heads far apart, tokens far apart
+        h = big.as_strided((1, 3, 3, 128), strides)
+        h.copy_(torch.randn(1, 3, 3, 128, generator=g).to(BF16))
+        codes = torch.empty(3, 384, dtype=torch.int8, device="cuda")
+        da.da_quantize_i8(h, codes, scale)
+        ref, m = oracle.row_codes(h.cpu().permute(0, 2, 1, 3).reshape(3, 384))
+        assert np.array_equal(codes.cpu().numpy().astype(np.int64), ref)
+        rope, near = da.Rope((44, 42, 42), (1, 1, 3)), torch.empty(1, 3, 3, 128, dtype=BF16, device="cuda")
+        da.da_rope(h, near, rope)
+        _rope_check(h, near, rope, None, None, 0, BF16)
+        da.da_rope(near, h, rope)
+        _rope_check(near, h.contiguous(), rope, None, None, 0, BF16)
+
+
+def test_strides_of_single_entries_do_not_matter():
+    """torch leaves any stride on a dimension of one entry."""
+    g = _gen(6)
+    x = torch.randn(1, 4, 40, 64, generator=g).to(BF16).cuda()
+    odd = x.as_strided(x.shape, (3, *x.stride()[1:]))
+    rope = da.Rope((20, 22, 22), (1, 5, 8))
+    a, b = torch.empty_like(x), torch.empty_like(x)
+    da.da_rope(x, a, rope)
+    da.da_rope(odd, b.as_strided(b.shape, (7, *b.stride()[1:])), rope)
+    assert torch.equal(a, b)
+    w, sw, s, ws = _codes(256, 64, 64, 1), _scales(256, 2).cuda(), _scales(40, 3).cuda(), torch.zeros(256, dtype=torch.uint8, device="cuda")
+    xq = _codes(40, 64, 64, 5)
+    da.da_linear_i8(xq, s, w, sw, a, ws)
+    da.da_linear_i8(xq, s, w, sw, b.as_strided(b.shape, (7, *b.stride()[1:])), ws)
+    assert torch.equal(a, b)
+
+
 @pytest.mark.parametrize("dtype", [BF16, F32])
 @pytest.mark.parametrize("B,H,N,d", [(1, 1, 1, 64), (2, 3, 37, 64), (1, 12, 130, 128), (3, 40, 5, 128), (2, 5, 19, 24), (1, 7, 3, 9)])
 def test_quantize_heads(B, H, N, d, dtype):
@@ -224,7 +304,7 @@ def _linear_close(got, x, sx, w, sw, bias, dtype):
 
 
 LINEAR = [(1, 1, 1), (1, 64, 16), (3, 17, 100), (16, 32, 128), (33, 257, 129), (64, 64, 1000), (127, 128, 256), (128, 129, 384),
-          (129, 255, 144), (200, 512, 640), (257, 640, 2048), (300, 96, 5120), (513, 1537, 1000), (1, 5120, 1536), (2, 2500, 1555), (5, 601, 4111), (7, 2401, 2048), (8, 2, 15), (1000, 40, 64),
+          (129, 255, 144), (200, 512, 640), (257, 640, 2048), (300, 96, 5120), (513, 1537, 1000), (1, 5120, 1536), (2, 2500, 1555), (5, 601, 4111), (7, 2401, 2048), (8, 2, 15), (1000, 40, 64), (9, 48, 131),
           (2, 30720, 256), (777, 3100, 72), (2049, 384, 128)]
 
 
@@ -378,6 +458,40 @@ def test_rope(B, H, N, d, axes, grid, norm, pairing, dtype):
     assert torch.equal(x, want) and torch.equal(buf[:, :, 0], before[:, :, 0])
 
 
+@pytest.mark.parametrize("B,N", [(300, 1), (65535, 1), (1, 1), (7, 33), (2, 4097)])
+def test_rope_of_many_and_of_single_tokens(B, N):
+    g = _gen(B)
+    x = torch.randn(B, 2, N, 64, generator=g).to(BF16).cuda()
+    out = torch.empty_like(x)
+    pos = torch.randint(0, 5000, (N, 3), generator=g, dtype=torch.int32).cuda()
+    rope = da.Rope((20, 22, 22), pairing="halves")
+    da.da_rope(x, out, rope, positions=pos)
+    _rope_check(x[:50], out[:50], rope, pos, None, 0, BF16)
+    one = torch.empty_like(x[-1:])
+    da.da_rope(x[-1:], one, rope, positions=pos)
+    assert torch.equal(one, out[-1:])
+
+
+def test_rope_at_the_ends_of_int32():
+    """Positions of the whole int32 range against whole-number arithmetic of the turns in Python."""
+    import math
+    from fractions import Fraction
+    x = torch.randn(1, 1, 4, 64, generator=_gen(3)).cuda()
+    pos = torch.tensor([[-(1 << 31)] * 3, [(1 << 31) - 1] * 3, [123456789, -987654321, 1], [0, 0, 0]], dtype=torch.int32)
+    out = torch.empty_like(x)
+    # theta = 1: every pair of an axis turns by the position in radians
+    da.da_rope(x, out, da.Rope((20, 22, 22), theta=1.0), positions=pos.cuda())
+    two_pi = Fraction(628318530717958647692528676655900576839, 10 ** 38)
+    ang = np.empty((4, 32))
+    for n in range(4):
+        for u, (lo, hi) in enumerate(((0, 10), (10, 21), (21, 32))):
+            p = Fraction(int(pos[n, u]))
+            ang[n, lo:hi] = float(p - two_pi * math.floor(p / two_pi))
+    ref = oracle.rope(x.cpu(), ang, False)
+    size = np.repeat(np.abs(_f64(x.cpu()))[..., 0::2] + np.abs(_f64(x.cpu()))[..., 1::2], 2, -1)
+    _close(out, ref, 2.0 ** -18 * size)
+
+
 def test_rope_far_positions_turn_as_the_formula_says():
     """Differences of positions: turning by p + q is turning by p, then by q; by -p undoes it."""
     g = _gen(1)
@@ -424,6 +538,28 @@ def _chain(seed, M=300, width=640, H=5, d=128):
         da.da_rope(s["h"], s["o"], rope)
         da.da_quantize_i8(s["o"], s["q2"], s["s2"])
     return s, run
+
+
+def test_two_chains_at_once():
+    """Two chains on two streams, issued in turns, without waiting: the bits of each alone."""
+    chains = [_chain(seed, M=2000 + 300 * seed) for seed in (3, 4)]
+    keys = ("sum", "q", "s", "h", "o", "q2", "s2")
+    want = []
+    for s, run in chains:
+        run()
+        torch.cuda.synchronize()
+        want.append({k: s[k].clone() for k in keys})
+        for k in keys:
+            s[k].zero_()
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in chains]
+    for _ in range(10):
+        for stream, (s, run) in zip(streams, chains):
+            with torch.cuda.stream(stream):
+                run()
+    torch.cuda.synchronize()
+    for (s, _), w in zip(chains, want):
+        assert all(torch.equal(s[k], w[k]) for k in keys) and da.da_device_status(s["ws"]) == 0
 
 
 def test_same_bits_on_streams_and_in_graphs():

@@ -11,7 +11,7 @@ from __future__ import annotations
 import ctypes
 import os
 from dataclasses import dataclass
-from typing import Optional, Tuple
+from typing import NamedTuple, Optional, Tuple
 
 import torch
 
@@ -60,8 +60,9 @@ class _HeadStrides(ctypes.Structure):
 
 
 class _RopePlan(ctypes.Structure):
-    _fields_ = [("axis_dims", ctypes.c_int * 3), ("grid", ctypes.c_int * 3), ("theta", ctypes.c_double),
-                ("pairing", ctypes.c_int)]
+    # the three entries of axis_dims and grid as fields of their own: quicker to fill than arrays
+    _fields_ = [(n, ctypes.c_int) for n in ("dims_t", "dims_h", "dims_w", "grid_t", "grid_h", "grid_w")] + [
+        ("theta", ctypes.c_double), ("pairing", ctypes.c_int)]
 
 
 _P = ctypes.c_void_p
@@ -484,12 +485,10 @@ def da_linear_i8(x: torch.Tensor, x_scale: torch.Tensor, w: torch.Tensor, w_scal
     return out
 
 
-_I3 = _I * 3
 PAIRINGS = {"adjacent": 0, "halves": 1}
 
 
-@dataclass(frozen=True)
-class Rope:
+class Rope(NamedTuple):
     """Rotary positions: the elements of a head that time, height and width turn, the token grid
     (unused where positions are given), the base of the frequencies and how pairs lie in a head."""
     axes: Tuple[int, int, int]
@@ -500,7 +499,7 @@ class Rope:
     def c(self) -> _RopePlan:
         if len(self.axes) != 3 or len(self.grid) != 3 or self.pairing not in PAIRINGS:
             raise DAError(_INVALID_ARG, "Rope: three axes, a grid of three and a pairing of " + " or ".join(PAIRINGS))
-        return _RopePlan(_I3(*self.axes), _I3(*self.grid), self.theta, PAIRINGS[self.pairing])
+        return _RopePlan(*self.axes, *self.grid, self.theta, PAIRINGS[self.pairing])
 
 
 def da_rope(x: torch.Tensor, out: torch.Tensor, rope: Rope, positions: Optional[torch.Tensor] = None,

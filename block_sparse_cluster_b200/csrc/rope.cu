@@ -344,11 +344,14 @@ cudaError_t launch_typed(RopeArgs& a, int B, cudaStream_t s) {
     threads = a.group = ((units + upt - 1) / upt + 31) / 32 * 32;
   }
   const int groups = threads / a.group;
-  // run: long enough to spread the angles over the threads and to keep loads ahead, short enough for the blocks to
-  // fill the GPU several times over
-  const long long tokens = (long long)B * a.N;
+  // run: long enough to spread the angles over the threads and to keep loads ahead, short enough for the blocks to fill the
+  // GPU several times over.  Blocks of many heads are few on an SM, so half as many fill it, and where the norm joins all
+  // their warps longer runs pay (40 heads: 255 us with 16 tokens, 267 with 8, 268 with 32; without the norm 239 with 8, 242
+  // with 16).
+  const long long tokens = (long long)B * a.N, blocks = 148 * (upt >= 2 && threads > 128 ? 8 : 16);
+  const int most = upt >= 2 && a.norm == kFullNorm ? 16 : 8;
   int per_group = 1;
-  while (per_group < 8 && groups * per_group * 2 <= kMaxRun && tokens / (groups * per_group * 2) >= 148 * 16) per_group *= 2;
+  while (per_group < most && groups * per_group * 2 <= kMaxRun && tokens / (groups * per_group * 2) >= blocks) per_group *= 2;
   a.run = groups * per_group;
   const dim3 grid((unsigned)((a.N + a.run - 1) / a.run), (unsigned)B, (unsigned)((a.H + a.heads_per_block - 1) / a.heads_per_block));
   return upt == 1   ? launch_units<T, D, 1>(a, grid, threads, s)

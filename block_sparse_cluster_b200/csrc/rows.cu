@@ -14,18 +14,22 @@
 // over the few elements within 2^-21 of it.
 //
 // A warp or a block owns a row and keeps it in registers between the reduction and the output, so every
-// input is read once and every output written once.  The bound is HBM, but instructions are close behind (for bf16
-// codes an SM has about 40 of them for each 32 elements at HBM's rate): arithmetic is done on packed pairs, codes are
+// input is read once and every output written once.  The bound is HBM, but instructions are close behind (at HBM's rate
+// an SM has 16 for each 32 elements of a bf16 row of codes): arithmetic is done on packed pairs, codes are
 // rounded by one addition, and a thread holds many elements so that a row's fixed work is spread.  Walking the rows
 // with as many blocks as the GPU holds, each row's loads ahead of the row in front, was slower (75600 x 5120 codes:
-// 338 us against 264; norm: 481 against 451): the registers of the loads ahead cost more warps than they hide.
+// 338 us against 264 then; norm: 481 against 451): the registers of the loads ahead cost more warps than they hide.
+//
+// Measured, bf16: norm with residual 75600 x 5120 451 us (6.86 TB/s, 1.07 of the plain copy's rate); codes of the norm with
+// residual 75600 x 1536 140 us (5.8 TB/s), x 5120 524 us (5.2 TB/s: two barriers a row, and a third for the 46 % of the
+// rows that need a second look); codes of 40 heads of 75600 tokens 200 us (5.8 TB/s).  Rows whose width or start is odd are
+// walked element by element, at a quarter to a half of these rates.
 #include "da_common.cuh"
 #include "da_internal.h"
 
 namespace da {
 
 namespace {
-
 
 enum { kNorm = 0, kNormI8 = 1, kQuantI8 = 2 };
 

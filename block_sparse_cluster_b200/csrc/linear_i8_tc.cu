@@ -350,13 +350,16 @@ linear_i8_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_const
       ok = __all_sync(0xffffffffu, ok && mbar_wait(&bars.acc_full[b], (n >> 1) & 1, abort, p.status));
       if (!ok) continue;
       tc_fence_after();
-      // a last part may reach beyond the tile: read, not stored; each part is read while the one before is stored
+      // a last part may reach beyond the tile: read, not stored; each part is read while the one before is stored, and
+      // waited for in the turn that asked for it
       const uint32_t acc = tmem + ((uint32_t)(ew * 32) << 16) + b * kMaxN;
       uint32_t r[32];
-      if (n0 + 32 * half < n1) tmem_ld32(acc + 32 * half, r);
+      if (n0 + 32 * half < n1) {
+        tmem_ld32(acc + 32 * half, r);
+        tmem_wait_ld_into(r);
+      }
 #pragma unroll 1
       for (int c0 = 32 * half; n0 + c0 < n1; c0 += 64) {
-        tmem_wait_ld_into(r);
         const ulonglong2* sw2 = reinterpret_cast<const ulonglong2*>(cs + c0);
         const ulonglong2* bi2 = reinterpret_cast<const ulonglong2*>(cs + kMaxN + c0);
         const uint64_t sx2 = f2_pack(sx, sx);
@@ -369,7 +372,8 @@ linear_i8_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_const
           f2_unpack(f2_fma(f2_mul(lo, sx2), w.x, bi.x), v[4 * i], v[4 * i + 1]);
           f2_unpack(f2_fma(f2_mul(hi, sx2), w.y, bi.y), v[4 * i + 2], v[4 * i + 3]);
         }
-        if (n0 + c0 + 64 < n1) tmem_ld32(acc + c0 + 64, r);
+        const bool more = n0 + c0 + 64 < n1;
+        if (more) tmem_ld32(acc + c0 + 64, r);
 #pragma unroll
         for (int g = 0; g < 32 / kSeg; ++g) {   // a segment of 64 bytes a row
           // row `lane`, 16-byte chunk j at chunk j ^ (row / 2 & 3): neither side of the transposition conflicts
@@ -422,6 +426,7 @@ linear_i8_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_const
           }
           __syncwarp();
         }
+        if (more) tmem_wait_ld_into(r);
       }
       tc_fence_before();
       __syncwarp();

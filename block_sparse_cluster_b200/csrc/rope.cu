@@ -158,35 +158,38 @@ __global__ void __launch_bounds__(512, UPT == 1 ? 2 : 1) rope_kernel(const __gri
   __shared__ int4 s_pos[kMaxRun];   // time, height, width, whether the token turns at all
   __shared__ uint64_t s_freq[D / 2];
   __shared__ unsigned char s_axis[D / 2];
-  __shared__ float s_part[2][16];
+  __shared__ __align__(16) float s_part[2][16];
   const int b = blockIdx.y, n0 = blockIdx.x * a.run, h0 = blockIdx.z * a.heads_per_block;
   const int run = min(a.run, a.N - n0);
   const int units = min(a.heads_per_block, a.H - h0) * kPerHead;
   const int groups = blockDim.x / a.group;
   const int g = threadIdx.x / a.group, gt = threadIdx.x - g * a.group;
   const int j = (gt % kPerHead) * V;    // the same for all units of a thread: group is a multiple of kPerHead
-  const T* x = static_cast<const T*>(a.x) + b * a.xb + (long long)h0 * a.xh + j;
-  T* out = static_cast<T*>(a.out) + b * a.ob + (long long)h0 * a.oh + j;
+  const T* x = static_cast<const T*>(a.x) + b * a.xb + (h0 + gt / kPerHead) * a.xh + j;
+  T* out = static_cast<T*>(a.out) + b * a.ob + (h0 + gt / kPerHead) * a.oh + j;
 
-  auto slot = [&](int it, int i, int q) { return s_ring + ((it % kStages * UPT + i) * 2 + q) * blockDim.x + threadIdx.x; };
-  auto fetch = [&](int it) {   // token g + it * groups of the run
-    const int k = g + it * groups;
+  // a thread's units lie the same number of heads apart in every token
+  const long long x_step = a.group / kPerHead * a.xh, out_step = a.group / kPerHead * a.oh;
+  auto has = [&](int i) { return gt + i * a.group < units; };
+  // the stage that is read next, and filled again; the token that is fetched next
+  uint4* const ring = s_ring + threadIdx.x;
+  const int vec = blockDim.x, stage = UPT * 2 * vec;
+  const T* next = x + (long long)(n0 + g) * a.xn;
+  const long long x_turn = groups * a.xn;
+  auto fetch = [&](int k, uint4* at) {   // token k of the run
     if (k < run) {
-      const T* p = x + (long long)(n0 + k) * a.xn;
 #pragma unroll
-      for (int i = 0; i < UPT; ++i) {
-        const int u = gt + i * a.group;
-        if (u < units) {
-          const T* e = p + (u / kPerHead) * a.xh;
-          cp_async16(slot(it, i, 0), e);
-          cp_async16(slot(it, i, 1), e + D / 2);
+      for (int i = 0; i < UPT; ++i)
+        if (has(i)) {
+          cp_async16(at + (2 * i) * vec, next + i * x_step);
+          cp_async16(at + (2 * i + 1) * vec, next + i * x_step + D / 2);
         }
-      }
     }
+    next += x_turn;
     cp_async_commit();
   };
 #pragma unroll
-  for (int it = 0; it < kStages; ++it) fetch(it);
+  for (int it = 0; it < kStages; ++it) fetch(g + it * groups, ring + it * stage);
 
   // weights of the thread's units, the same for every token
   uint4 wraw[NORMED ? UPT : 1][2];
@@ -214,6 +217,7 @@ __global__ void __launch_bounds__(512, UPT == 1 ? 2 : 1) rope_kernel(const __gri
       s_pos[k] = make_int4((int)t, (int)(line - t * a.grid[1]), (int)(n - line * a.grid[2]), t < (unsigned)a.grid[0]);
     }
   }
+  if (threadIdx.x < 32) (&s_part[0][0])[threadIdx.x] = 0.f;
   for (int p = threadIdx.x; p < D / 2; p += blockDim.x) {
     s_freq[p] = a.freq[p];
     s_axis[p] = a.axis[p];
@@ -228,16 +232,22 @@ __global__ void __launch_bounds__(512, UPT == 1 ? 2 : 1) rope_kernel(const __gri
   __syncthreads();
 
   // every group takes the same number of turns, so that the barriers match
-  for (int k0 = 0, it = 0; k0 < run; k0 += groups, ++it) {
+  uint4 raw[UPT][2];
+#pragma unroll
+  for (int i = 0; i < UPT; ++i) raw[i][0] = raw[i][1] = make_uint4(0, 0, 0, 0);   // stays so for units the thread lacks
+  uint4* at = ring;
+  T* o = out + (long long)(n0 + g) * a.on;
+  const long long out_turn = groups * a.on;
+  for (int k0 = 0, parity = 0; k0 < run; k0 += groups, parity ^= 1, o += out_turn) {
     const int k = k0 + g;
-    uint4 raw[UPT][2];
     float ss = 0.f, factor[UPT];
     cp_async_wait<kStages - 1>();
 #pragma unroll
     for (int i = 0; i < UPT; ++i) {
-      const bool mine = k < run && gt + i * a.group < units;
-      raw[i][0] = mine ? *slot(it, i, 0) : make_uint4(0, 0, 0, 0);
-      raw[i][1] = mine ? *slot(it, i, 1) : make_uint4(0, 0, 0, 0);
+      if (has(i)) {   // behind the run's end, what an earlier turn left: worked on, not stored
+        raw[i][0] = at[(2 * i) * vec];
+        raw[i][1] = at[(2 * i + 1) * vec];
+      }
       factor[i] = 1.f;
       if (NORMED) {
         uint64_t va[V / 2], vb[V / 2], s2 = 0;
@@ -259,20 +269,20 @@ __global__ void __launch_bounds__(512, UPT == 1 ? 2 : 1) rope_kernel(const __gri
       }
     } else if (NORMED) {
       for (int o = min(a.group, 32) / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-      if (a.group > 32) {
-        if ((threadIdx.x & 31) == 0) s_part[it & 1][threadIdx.x >> 5] = ss;
+      if (a.group > 32) {   // the block is the group: its warps' sums, in order; warps it lacks have left zeros
+        if ((threadIdx.x & 31) == 0) s_part[parity][threadIdx.x >> 5] = ss;
         __syncthreads();
-        ss = (threadIdx.x & 31) < (blockDim.x >> 5) ? s_part[it & 1][threadIdx.x & 31] : 0.f;
-#pragma unroll
-        for (int o = 8; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-        ss = __shfl_sync(0xffffffffu, ss, 0);
+        ss = 0.f;
+        for (int w = 0; w < blockDim.x >> 5; w += 4) {
+          const float4 p = *reinterpret_cast<const float4*>(&s_part[parity][w]);
+          ss += (p.x + p.y) + (p.z + p.w);
+        }
       }
       const float f = rsqrtf(ss * a.inv_width + a.eps);
 #pragma unroll
       for (int i = 0; i < UPT; ++i) factor[i] = f;
     }
     if (k < run) {
-      T* o = out + (long long)(n0 + k) * a.on;
       const bool turn = s_pos[k].w != 0;
       // halves: pairs j .. j + V; adjacent: V / 2 pairs of each vector
       uint64_t c[V / 2], s[V / 2];
@@ -290,8 +300,7 @@ __global__ void __launch_bounds__(512, UPT == 1 ? 2 : 1) rope_kernel(const __gri
       }
 #pragma unroll
       for (int i = 0; i < UPT; ++i) {
-        const int u = gt + i * a.group;
-        if (u >= units) continue;
+        if (!has(i)) continue;
         uint64_t va[V / 2], vb[V / 2];
         U::unpack(raw[i], va, vb);
         if (NORMED) {
@@ -307,12 +316,13 @@ __global__ void __launch_bounds__(512, UPT == 1 ? 2 : 1) rope_kernel(const __gri
         if (turn) U::rotate(va, vb, c, s);   // a token that does not turn is copied, whatever it holds
         uint4 o2[2];
         U::pack(va, vb, o2);
-        T* e = o + (long long)(u / kPerHead) * a.oh;
+        T* e = o + i * out_step;
         *reinterpret_cast<uint4*>(e) = o2[0];
         *reinterpret_cast<uint4*>(e + D / 2) = o2[1];
       }
     }
-    fetch(it + kStages);   // into the slots that this turn has read
+    fetch(k + kStages * groups, at);   // into the stage that this turn has read
+    at = at == ring + (kStages - 1) * stage ? ring : at + stage;
   }
 }
 

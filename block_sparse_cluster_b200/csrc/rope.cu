@@ -16,8 +16,8 @@
 // of tokens: the block forms the angles of all of them first, and each thread keeps the loads of the next kStages tokens
 // in flight with cp.async, into shared memory that only it reads: loads ahead cost no registers and need no barrier.
 //
-// Measured, bf16, 40 heads of 128 and 75600 tokens (floor 241 us): 239 us without a norm, 240 with the head's, 255 with the
-// norm over all heads, whose barrier a token is what is left; 12 heads, 32760 tokens (floor 31 us): 34, 38 and 46 us, where
+// Measured, bf16, 40 heads of 128 and 75600 tokens (floor 241 us): 239 us without a norm, 245 with the head's, 247 with the
+// norm over all heads, whose barrier a token is what is left; 12 heads, 32760 tokens (floor 31 us): 35, 37 and 42 us, where
 // a token is 96 threads' work of 16 elements and its fixed instructions show.  fp32 runs at the copy's rate.
 #include <math.h>
 
@@ -148,7 +148,7 @@ struct Unit<float, HALVES> {
 
 // UPT: units a thread holds of a token.
 template <typename T, int D, int UPT, bool HALVES, bool NORMED>
-__global__ void __launch_bounds__(512, UPT == 1 ? 2 : 1) rope_kernel(const __grid_constant__ RopeArgs a) {
+__global__ void __launch_bounds__(512) rope_kernel(const __grid_constant__ RopeArgs a) {
   using U = Unit<T, HALVES>;
   constexpr int V = U::n;
   constexpr int kPerHead = D / 2 / V;   // units of a head
@@ -328,8 +328,10 @@ __global__ void __launch_bounds__(512, UPT == 1 ? 2 : 1) rope_kernel(const __gri
 
 template <typename T, int D, int UPT>
 cudaError_t launch_units(const RopeArgs& a, dim3 grid, int threads, cudaStream_t s) {
-  auto kernel = a.halves ? (a.norm ? rope_kernel<T, D, UPT, true, true> : rope_kernel<T, D, UPT, true, false>)
-                         : (a.norm ? rope_kernel<T, D, UPT, false, true> : rope_kernel<T, D, UPT, false, false>);
+  auto kernel = a.halves ? rope_kernel<T, D, UPT, true, false> : rope_kernel<T, D, UPT, false, false>;
+  // a norm comes with one or two units, and with four of the widest fp32 tokens
+  if constexpr (UPT <= 2 || (UPT == 4 && sizeof(T) == 4))
+    if (a.norm) kernel = a.halves ? rope_kernel<T, D, UPT, true, true> : rope_kernel<T, D, UPT, false, true>;
   const size_t smem = (size_t)kStages * UPT * 2 * threads * 16 + (size_t)a.run * D * 4;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
@@ -346,7 +348,7 @@ cudaError_t launch_typed(RopeArgs& a, int B, cudaStream_t s) {
   int threads, upt;
   // Few units: a warp, or less, a token, so that a sum stays in it; the norm's weights leave room for two units a thread.
   // More: a block a token, one unit a thread while that fills few warps, since registers are what bounds the warps of an
-  // SM (bf16, 12 heads of 128, head norm: 40 us against 45 with three units in a warp; 16 heads: 79 against 158), two or
+  // SM (bf16, 12 heads of 128, head norm: 37 us against 45 with three units in a warp; 16 heads: 79 against 158), two or
   // four where the barrier of the norm over all heads would join many warps (40 heads, runs of 8: 269 us against 296 with one).
   if (units <= (a.norm == kNoNorm ? 128 : 64)) {
     a.group = kPerHead;

@@ -143,11 +143,12 @@ struct RowArgs {
   long long x_batch, x_head, x_token, r_stride, sum_stride, out_stride;
   float eps, inv_width;
   long long x_step;       // from a thread's vector of x to its next one, or -1 where that is not the same for all
+  uint32_t per_head;      // ceil(2^32 / head_dim): columns and head_dim are at most 2^14, so column * per_head >> 32 is the head
 };
 
 // Element c of a row of x.
 __device__ __forceinline__ long long x_offset(const RowArgs& a, int c) {
-  const int h = c / a.head_dim;
+  const int h = a.head_dim == 1 ? c : (int)__umulhi((uint32_t)c, a.per_head);
   return h * a.x_head + (c - h * a.head_dim);
 }
 
@@ -539,6 +540,9 @@ cudaError_t launch_rows_t(const RowArgs& a, cudaStream_t s) {
   return vec ? launch_rows_v<T, V, MODE>(a, s) : launch_rows_v<T, 1, MODE>(a, s);
 }
 
+// The reciprocal that x_offset multiplies by; a head of one element needs none (2^32 does not fit).
+uint32_t per_head(int d) { return d == 1 ? 0u : (uint32_t)(((1ull << 32) + d - 1) / d); }
+
 template <int MODE>
 cudaError_t launch_rows(bool bf16, const RowArgs& a, cudaStream_t s) {
   return bf16 ? launch_rows_t<__nv_bfloat16, 8, MODE>(a, s) : launch_rows_t<float, 4, MODE>(a, s);
@@ -550,14 +554,14 @@ cudaError_t launch_rms_norm(bool bf16, long long rows, int width, const void* x,
                             const void* residual, long long r_stride, const void* weight, float eps, void* sum_out,
                             long long sum_stride, void* out, long long out_stride, float* scale, cudaStream_t s) {
   const RowArgs a{x, residual, weight, sum_out, out, scale, rows, width, width, (int)rows,
-                  0, 0, x_stride, r_stride, sum_stride, out_stride, eps, 1.f / (float)width, 0};
+                  0, 0, x_stride, r_stride, sum_stride, out_stride, eps, 1.f / (float)width, 0, per_head(width)};
   return scale ? launch_rows<kNormI8>(bf16, a, s) : launch_rows<kNorm>(bf16, a, s);
 }
 
 cudaError_t launch_quantize_i8(bool bf16, int B, int H, int N, int d, const void* x, const da_head_strides& xs,
                                int8_t* q, long long q_stride, float* scale, cudaStream_t s) {
   const RowArgs a{x, nullptr, nullptr, nullptr, q, scale, (long long)B * N, H * d, d, N,
-                  xs.batch, xs.head, xs.token, 0, 0, q_stride, 0.f, 1.f, 0};
+                  xs.batch, xs.head, xs.token, 0, 0, q_stride, 0.f, 1.f, 0, per_head(d)};
   return launch_rows<kQuantI8>(bf16, a, s);
 }
 

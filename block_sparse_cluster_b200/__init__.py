@@ -326,87 +326,16 @@ def da_noalloc_device_status(stream=None) -> int:
     return _lib.da_noalloc_device_status(_stream(stream))
 
 
-# Operators of the layer around the attention.  They take strided tensors, so the binding also reads
-# shapes, strides and devices; the calls run on the tensors' device, on its current stream by default.
+# Operators of the layer around the attention.  They take strided tensors, so their marshalling also reads
+# shapes, strides and devices, in a compiled module (csrc/layer_call.cpp), since the smallest of these calls are bound by
+# the host.  They run on the tensors' device, on its current stream by default.
 
-_CODES = {torch.bfloat16: DA_BF16, torch.float32: DA_F32}
-_INVALID_ARG, _SHAPE, _DTYPE = 1, 2, 3
-
-
-def _refuse(code: int, where: str, what: str):
-    raise DAError(code, f"{where}: {what}")
-
-
-def _device(where: str, *tensors: Optional[torch.Tensor]) -> int:
-    """The one CUDA device that holds all the tensors."""
-    device = tensors[0].get_device()
-    for t in tensors:
-        if t is not None and (t.get_device() != device or device < 0):
-            _refuse(_INVALID_ARG, where, "tensors have to be on one CUDA device")
-    return device
-
-
-def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
-    return None if t is None else t.data_ptr()
-
-
-def _code(t: torch.Tensor, where: str, what: str) -> int:
-    if t.dtype not in _CODES:
-        _refuse(_DTYPE, where, what + " has to be bfloat16 or float32")
-    return _CODES[t.dtype]
-
-
-def _rows(t: torch.Tensor, rows: int, width: int, dtype, where: str, what: str) -> int:
-    """The row stride of a [rows, width] tensor with contiguous rows."""
-    if t.shape != (rows, width):
-        _refuse(_SHAPE, where, f"{what} has to be [{rows}, {width}]")
-    if t.dtype != dtype:
-        _refuse(_DTYPE, where, f"{what} has to be {dtype}")
-    stride, inner = t.stride()
-    if inner != 1 and width > 1:
-        _refuse(_SHAPE, where, f"{what} needs contiguous rows")
-    return stride if rows > 1 else max(width, stride)
-
-
-def _vector(t: torch.Tensor, n: int, dtype, where: str, what: str):
-    if t.shape != (n,):
-        _refuse(_SHAPE, where, f"{what} has to be [{n}]")
-    if t.dtype != dtype:
-        _refuse(_DTYPE, where, f"{what} has to be {dtype}")
-    if n > 1 and t.stride(0) != 1:
-        _refuse(_SHAPE, where, f"{what} has to be contiguous")
-
-
-def _head_strides(t: torch.Tensor, where: str, what: str) -> _HeadStrides:
-    """Strides of a [B, H, N, d] tensor with contiguous heads."""
-    if t.dim() != 4:
-        _refuse(_SHAPE, where, f"{what} has to be [B, H, N, d]")
-    batch, head, token, inner = t.stride()
-    if inner != 1 and t.shape[3] > 1:
-        _refuse(_SHAPE, where, f"{what} needs a contiguous last dimension")
-    return _HeadStrides(batch, head, token)
-
-
-def _on(device: int, stream, f, *args) -> int:
-    """f(*args, stream) with `device` current; the stream is the device's current one by default."""
-    # the raw calls cost a tenth of torch.cuda's, which matters for the smallest operators
-    raw = torch._C._cuda_getCurrentRawStream(device) if stream is None else _stream(stream)
-    if device == torch._C._cuda_getDevice():
-        return f(*args, raw)
-    with torch.cuda.device(device):
-        return f(*args, raw)
-
-
-def _norm_args(where, x, weight, residual, sum_out, eps):
-    code = _code(x, where, "x")
-    if x.dim() != 2:
-        _refuse(_SHAPE, where, "x has to be [rows, width]")
-    rows, width = x.shape
-    if weight is not None:
-        _vector(weight, width, x.dtype, where, "weight")
-    return (rows, width, code, x.data_ptr(), _rows(x, rows, width, x.dtype, where, "x"), _ptr(residual),
-            0 if residual is None else _rows(residual, rows, width, x.dtype, where, "residual"), _ptr(weight), eps,
-            _ptr(sum_out), 0 if sum_out is None else _rows(sum_out, rows, width, x.dtype, where, "sum_out"))
+try:
+    from . import _layer_call
+except ImportError as e:
+    raise ImportError("_layer_call.so is not built or does not load; run python block_sparse_cluster_b200/build.py") from e
+_layer_call.bind(DAError, {name: ctypes.cast(getattr(_lib, name), _P).value for name in
+                           ("da_rms_norm", "da_rms_norm_i8", "da_quantize_i8", "da_linear_i8", "da_rope")})
 
 
 def da_rms_norm(x: torch.Tensor, weight: Optional[torch.Tensor], out: torch.Tensor,
@@ -414,42 +343,24 @@ def da_rms_norm(x: torch.Tensor, weight: Optional[torch.Tensor], out: torch.Tens
                 stream=None) -> torch.Tensor:
     """out = v / sqrt(mean(v^2) + eps) * weight with v = x + residual, rows [rows, width] of bf16 or
     fp32; sum_out takes v (the residual stream; it may be the residual's or x's own buffer)."""
-    where = "da_rms_norm"
-    device = _device(where, x, weight, out, residual, sum_out)
-    _check(_on(device, stream, _lib.da_rms_norm, *_norm_args(where, x, weight, residual, sum_out, eps), out.data_ptr(),
-               _rows(out, x.shape[0], x.shape[1], x.dtype, where, "out")), where)
+    _layer_call.rms_norm(x, weight, out, residual, sum_out, eps, stream)
     return out
 
 
 def da_rms_norm_i8(x: torch.Tensor, weight: Optional[torch.Tensor], q: torch.Tensor, scale: torch.Tensor,
                    residual: Optional[torch.Tensor] = None, sum_out: Optional[torch.Tensor] = None, eps: float = 1e-6,
-                   stream=None):
+                   stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
     """da_rms_norm with its output in 8-bit codes: q [rows, width] int8 (rows may be padded: a row
     stride that is a multiple of 16 suits da_linear_i8), scale [rows] fp32, output = q * scale."""
-    where = "da_rms_norm_i8"
-    device = _device(where, x, weight, q, scale, residual, sum_out)
-    args = _norm_args(where, x, weight, residual, sum_out, eps)
-    _vector(scale, x.shape[0], torch.float32, where, "scale")
-    _check(_on(device, stream, _lib.da_rms_norm_i8, *args, q.data_ptr(),
-               _rows(q, x.shape[0], x.shape[1], torch.int8, where, "q"), scale.data_ptr()), where)
+    _layer_call.rms_norm_i8(x, weight, q, scale, residual, sum_out, eps, stream)
     return q, scale
 
 
-def da_quantize_i8(x: torch.Tensor, q: torch.Tensor, scale: torch.Tensor, stream=None):
+def da_quantize_i8(x: torch.Tensor, q: torch.Tensor, scale: torch.Tensor,
+                   stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
     """Rows in 8-bit codes with a scale each, x ~ q * scale: x is [rows, width], or the attention's
     [B, H, N, d], whose token (b, n) becomes row b * N + n of q [B*N, H*d] (heads side by side)."""
-    where = "da_quantize_i8"
-    device = _device(where, x, q, scale)
-    code = _code(x, where, "x")
-    if x.dim() == 2:
-        B, H, (N, d) = 1, 1, x.shape
-        strides = _HeadStrides(0, 0, _rows(x, N, d, x.dtype, where, "x"))
-    else:
-        strides = _head_strides(x, where, "x")
-        B, H, N, d = x.shape
-    _vector(scale, B * N, torch.float32, where, "scale")
-    _check(_on(device, stream, _lib.da_quantize_i8, B, H, N, d, code, x.data_ptr(), ctypes.byref(strides),
-               q.data_ptr(), _rows(q, B * N, H * d, torch.int8, where, "q"), scale.data_ptr()), where)
+    _layer_call.quantize_i8(x, q, scale, stream)
     return q, scale
 
 
@@ -458,34 +369,8 @@ def da_linear_i8(x: torch.Tensor, x_scale: torch.Tensor, w: torch.Tensor, w_scal
     """out = (x w^T) * x_scale * w_scale + bias for int8 codes x [M, K] and w [C, K], fp32 scales [M]
     and [C], fp32 bias [C]; out is [M, C] or, as heads, [B, H, N, d] with B*N = M, H*d = C, of bf16 or
     fp32.  ws: a zero-filled workspace of at least 256 bytes (one of `workspace(dims)` serves too)."""
-    where = "da_linear_i8"
-    device = _device(where, x, x_scale, w, w_scale, out, ws, bias)
-    code = _code(out, where, "out")
-    if x.dim() != 2 or w.dim() != 2:
-        _refuse(_SHAPE, where, "x and w have to be matrices")
-    (M, K), C = x.shape, w.shape[0]
-    if out.dim() == 2:
-        B, H, N, d = 1, 1, M, C
-        strides = _HeadStrides(0, 0, _rows(out, M, C, out.dtype, where, "out"))
-    else:
-        strides = _head_strides(out, where, "out")
-        B, H, N, d = out.shape
-        if B * N != M or H * d != C:
-            _refuse(_SHAPE, where, f"out has to hold {M} tokens of {C} channels")
-    _vector(x_scale, M, torch.float32, where, "x_scale")
-    _vector(w_scale, C, torch.float32, where, "w_scale")
-    if bias is not None:
-        _vector(bias, C, torch.float32, where, "bias")
-    if not ws.is_contiguous():
-        _refuse(_SHAPE, where, "ws has to be contiguous")
-    _check(_on(device, stream, _lib.da_linear_i8, B, N, H, d, K, x.data_ptr(), _rows(x, M, K, torch.int8, where, "x"),
-               x_scale.data_ptr(), w.data_ptr(), _rows(w, C, K, torch.int8, where, "w"), w_scale.data_ptr(),
-               _ptr(bias), code, out.data_ptr(), ctypes.byref(strides), ws.data_ptr(),
-               ws.numel() * ws.element_size()), where)
+    _layer_call.linear_i8(x, x_scale, w, w_scale, out, ws, bias, stream)
     return out
-
-
-PAIRINGS = {"adjacent": 0, "halves": 1}
 
 
 class Rope(NamedTuple):
@@ -496,39 +381,13 @@ class Rope(NamedTuple):
     theta: float = 10000.0
     pairing: str = "adjacent"
 
-    def c(self) -> _RopePlan:
-        if len(self.axes) != 3 or len(self.grid) != 3 or self.pairing not in PAIRINGS:
-            raise DAError(_INVALID_ARG, "Rope: three axes, a grid of three and a pairing of " + " or ".join(PAIRINGS))
-        return _RopePlan(*self.axes, *self.grid, self.theta, PAIRINGS[self.pairing])
-
 
 def da_rope(x: torch.Tensor, out: torch.Tensor, rope: Rope, positions: Optional[torch.Tensor] = None,
             weight: Optional[torch.Tensor] = None, eps: float = 1e-6, stream=None) -> torch.Tensor:
     """Rotary positions of x [B, H, N, d] (any strides with contiguous heads, such as a view of a
     projection's token rows) into out, which may be x.  positions: int32 [N, 3] or [B, N, 3]; None:
     the rope's grid.  weight [d] or [H*d]: the head or the token is normed first."""
-    where = "da_rope"
-    device = _device(where, x, out, positions, weight)
-    code = _code(x, where, "x")
-    if out.dtype != x.dtype:
-        _refuse(_DTYPE, where, "out has to be of x's type")
-    xs, os_ = _head_strides(x, where, "x"), _head_strides(out, where, "out")
-    if out.shape != x.shape:
-        _refuse(_SHAPE, where, "out has to be of x's shape")
-    B, H, N, d = x.shape
-    batch = width = 0
-    if positions is not None:
-        if positions.dtype != torch.int32:
-            _refuse(_DTYPE, where, "positions have to be int32")
-        if positions.shape not in ((N, 3), (B, N, 3)) or not positions.is_contiguous():
-            _refuse(_SHAPE, where, f"positions have to be contiguous [{N}, 3] or [{B}, {N}, 3]")
-        batch = 3 * N if positions.dim() == 3 else 0
-    if weight is not None:
-        width = weight.numel()
-        _vector(weight, width, x.dtype, where, "weight")
-    _check(_on(device, stream, _lib.da_rope, ctypes.byref(rope.c()), B, H, N, d, code, x.data_ptr(),
-               ctypes.byref(xs), _ptr(positions), batch, _ptr(weight), width, eps, out.data_ptr(),
-               ctypes.byref(os_)), where)
+    _layer_call.rope(x, out, rope, positions, weight, eps, stream)
     return out
 
 

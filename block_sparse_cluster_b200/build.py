@@ -6,9 +6,11 @@
 """
 import concurrent.futures as cf
 import glob
+import importlib.util
 import os
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -16,6 +18,8 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libda.so")
 FAULT_LIB = os.path.join(HERE, "libda_fault.so")
+CALL_SRC = os.path.join(CSRC, "layer_call.cpp")
+CALL_LIB = os.path.join(HERE, "_layer_call.so")
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-fvisibility=hidden",
@@ -45,9 +49,24 @@ def _link(objs, lib):
         raise RuntimeError(f"nvcc link of {os.path.basename(lib)} failed")
 
 
+def build_call():
+    """Compile the layer operators' marshalling module (host code against torch's and Python's headers)."""
+    torch = os.path.dirname(importlib.util.find_spec("torch").origin)
+    cuda = os.path.dirname(os.path.dirname(NVCC))
+    cmd = ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden",
+           *["-I" + d for d in (os.path.join(ROOT, "include"), os.path.join(torch, "include"),
+                                os.path.join(torch, "include", "torch", "csrc", "api", "include"),
+                                sysconfig.get_paths()["include"], os.path.join(cuda, "include"))],
+           CALL_SRC, "-o", CALL_LIB, "-L" + os.path.join(torch, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        sys.stderr.write(r.stdout + r.stderr)
+        raise RuntimeError("g++ failed: layer_call.cpp")
+
+
 def build(verbose=False, force=False, extra=()):
-    """Compile every csrc/*.cu for sm_100a and link libda.so, and the test build libda_fault.so
-    (the same sources with DA_FAULT_INJECT defined: one withheld barrier arrival, for the test of
+    """Compile every csrc/*.cu for sm_100a and link libda.so, the layer operators' marshalling module
+    _layer_call.so, and the test build libda_fault.so (the same sources with DA_FAULT_INJECT defined: one withheld barrier arrival, for the test of
     the bounded device waits); skip what is up to date."""
     os.makedirs(BUILD, exist_ok=True)
     deps = _deps_mtime()
@@ -62,6 +81,8 @@ def build(verbose=False, force=False, extra=()):
         if failed:
             raise RuntimeError("nvcc failed: " + ", ".join(os.path.basename(f[0]) for f in failed))
         _link([r[1] for r in results], LIB)
+    if force or not os.path.exists(CALL_LIB) or os.path.getmtime(CALL_LIB) < deps:
+        build_call()
     if force or not os.path.exists(FAULT_LIB) or os.path.getmtime(FAULT_LIB) < deps:
         # only the attention kernel differs in the test build
         src = os.path.join(CSRC, "attention_tc.cu")

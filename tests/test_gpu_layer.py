@@ -599,3 +599,72 @@ def test_same_bits_on_streams_and_in_graphs():
     run_t()
     torch.cuda.synchronize()
     assert da.da_device_status(s["ws"]) == 0 and da.da_device_status(t["ws"]) == 0
+
+
+# ---------------------------------------------------------------------------
+# what the binding refuses by shape, type and stride
+
+def _refused(code, f, *args, **kw):
+    with pytest.raises(da.DAError) as e:
+        f(*args, **kw)
+    assert e.value.code == code, str(e.value)
+
+
+def test_binding_refuses_shapes_types_and_strides():
+    SHAPE, DTYPE, INVALID = 2, 3, 1
+    x, w = torch.zeros(4, 64, device="cuda"), torch.zeros(64, device="cuda")
+    q, s, ws = torch.zeros(4, 64, dtype=torch.int8, device="cuda"), torch.zeros(4, device="cuda"), torch.zeros(256, dtype=torch.uint8, device="cuda")
+    b = x.to(BF16)
+    _refused(DTYPE, da.da_rms_norm, x.half(), None, x)
+    _refused(DTYPE, da.da_rms_norm, x, None, b)
+    _refused(DTYPE, da.da_rms_norm, x, w.to(BF16), x)
+    _refused(SHAPE, da.da_rms_norm, x, w[:63], x)
+    _refused(SHAPE, da.da_rms_norm, x, w[None], x)
+    _refused(SHAPE, da.da_rms_norm, x, None, x[:3])
+    _refused(SHAPE, da.da_rms_norm, x, None, x.t())
+    _refused(SHAPE, da.da_rms_norm, x[None], None, x[None])
+    _refused(SHAPE, da.da_rms_norm, x, None, torch.empty(64, 4, device="cuda").t())
+    _refused(SHAPE, da.da_rms_norm, x, None, x, residual=x[:, :63])
+    _refused(INVALID, da.da_rms_norm, x, None, x.cpu())
+    _refused(INVALID, da.da_rms_norm, x, None, torch.empty_like(x), sum_out=x)      # a sum without a residual
+    _refused(INVALID, da.da_rms_norm, x[:0], None, x[:0])
+    _refused(DTYPE, da.da_rms_norm_i8, x, None, x, s)
+    _refused(SHAPE, da.da_rms_norm_i8, x, None, q, s[:3])
+    _refused(DTYPE, da.da_quantize_i8, q, q, s)
+    _refused(SHAPE, da.da_quantize_i8, x.view(2, 2, 64), q, s)
+    _refused(SHAPE, da.da_quantize_i8, x.view(1, 2, 2, 64), q, s)
+    _refused(SHAPE, da.da_linear_i8, q, s, q, s, x, ws)                             # out is [4, 64], not [4, 4]
+    _refused(DTYPE, da.da_linear_i8, q, s, q, s, torch.zeros(4, 4, dtype=torch.int32, device="cuda"), ws)
+    _refused(SHAPE, da.da_linear_i8, q, s, q, s, torch.zeros(1, 2, 4, 4, device="cuda"), ws)
+    _refused(9, da.da_linear_i8, q, s, q, s, torch.zeros(4, 4, device="cuda"), ws[:255])
+    _refused(SHAPE, da.da_linear_i8, q, s, q, s, torch.zeros(4, 4, device="cuda"), ws.repeat(2)[::2])
+    h, rope = torch.zeros(1, 1, 4, 64, device="cuda"), da.Rope((32, 16, 16), (1, 2, 2))
+    o = torch.empty_like(h)
+    _refused(SHAPE, da.da_rope, h[0], o[0], rope)
+    _refused(SHAPE, da.da_rope, h, o[:, :, :3], rope)
+    _refused(DTYPE, da.da_rope, h, o.to(BF16), rope)
+    _refused(DTYPE, da.da_rope, h, o, rope, positions=torch.zeros(4, 3, dtype=torch.int64, device="cuda"))
+    _refused(SHAPE, da.da_rope, h, o, rope, positions=torch.zeros(3, 3, dtype=torch.int32, device="cuda"))
+    _refused(SHAPE, da.da_rope, h, o, rope, weight=torch.zeros(65, device="cuda"))
+    _refused(SHAPE, da.da_rope, h, o, da.Rope((32, 16, 16)))                        # neither a grid nor positions
+    with pytest.raises(TypeError):
+        da.da_rms_norm(x, None, torch.empty_like(x), eps="small")
+    with pytest.raises(TypeError):
+        da.da_rope(h, o, da.Rope((32, 16, 16), (1, 2, 2), theta="large"))
+
+
+def test_stream_arguments():
+    """A stream object, its handle and the current stream are the same to a call."""
+    x = torch.randn(64, 256, generator=_gen(1)).cuda()
+    want, out = torch.empty_like(x), torch.empty_like(x)
+    da.da_rms_norm(x, None, want)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for stream in (side, side.cuda_stream):
+        out.zero_()
+        torch.cuda.synchronize()
+        da.da_rms_norm(x, None, out, stream=stream)
+        side.synchronize()
+        assert torch.equal(out, want)
+    with pytest.raises(TypeError):
+        da.da_rms_norm(x, None, out, stream="side")

@@ -120,7 +120,28 @@ def test_binding_refuses_before_the_library():
         with pytest.raises(da.DAError) as e:
             f()
         assert e.value.code == INVALID
-    with pytest.raises(da.DAError):
-        da.Rope((32, 16, 16), pairing="other").c()
-    with pytest.raises(da.DAError):
-        da.Rope((32, 32)).c()
+    h = x.view(1, 1, 4, 64)
+    for rope, word in ((da.Rope((32, 16, 16), pairing="other"), "pairing"), (da.Rope((32, 32)), "axes"),
+                       (da.Rope((32, 16, 16), (1, 2)), "grid"), (da.Rope((32, 16, 1 << 40)), "axes"), ((1, 2), "Rope")):
+        with pytest.raises(da.DAError, match=word) as e:
+            da.da_rope(h, h, rope)
+        assert e.value.code == INVALID
+    for bad in (lambda: da.da_rms_norm(1, None, x), lambda: da.da_quantize_i8(x, None, s), lambda: da.da_rope(h, [], da.Rope((32, 16, 16)))):
+        with pytest.raises(da.DAError) as e:
+            bad()
+        assert e.value.code == INVALID
+
+
+def test_package_fails_loudly_without_the_marshalling_module(tmp_path):
+    import os
+    import shutil
+    import subprocess
+    import sys
+    src = os.path.dirname(da.LIB_PATH)
+    pkg = tmp_path / "block_sparse_cluster_b200"
+    pkg.mkdir()
+    for name in ("__init__.py", "layer.py", "libda.so"):
+        shutil.copy(os.path.join(src, name), pkg / name)
+    r = subprocess.run([sys.executable, "-c", "import block_sparse_cluster_b200"], cwd=tmp_path,
+                       env={**os.environ, "PYTHONPATH": str(tmp_path)}, capture_output=True, text=True, timeout=300)
+    assert r.returncode != 0 and "ImportError" in r.stderr and "_layer_call.so is not built" in r.stderr

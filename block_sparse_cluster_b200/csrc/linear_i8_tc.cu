@@ -416,6 +416,7 @@ linear_i8_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_const
             const int col = lane % kSeg, c = s0 + col, h = c / A.d;
             const long long head = h * A.out_head + (c - h * A.d);
             const int byte = col * (int)sizeof(T);
+#pragma unroll 8
             for (int i = 0; i < 32; i += kRows) {
               const int row = i + lane / kSeg;
               const long long ro = __shfl_sync(0xffffffffu, off, row);

@@ -505,7 +505,7 @@ da_status da_linear_i8(int B, int N, int H, int d, int K, const int8_t* x, int64
                      x_stride, w_stride, os.batch, os.head, os.token};
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const bool bf16 = out_dtype == DA_BF16;
-  if (!linear_i8_tc_supported(a)) return cuda_status(launch_linear_i8_simt(bf16, a, s));
+  if (!linear_i8_tc_supported(a)) return cuda_status(launch_linear_i8_bytes(bf16, a, static_cast<int*>(ws), s));
   if (linear_i8_rows_supported(a)) return cuda_status(launch_linear_i8_rows(bf16, a, s));
   return cuda_status(launch_linear_i8_tc(bf16, a, static_cast<int*>(ws), s));
 }

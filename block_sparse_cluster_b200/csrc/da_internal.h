@@ -79,7 +79,7 @@ cudaError_t launch_rope(bool bf16, const da_rope_plan& plan, int B, int H, int N
                         const da_head_strides& xs, const int32_t* positions, long long pos_batch, const void* weight,
                         int weight_width, float eps, void* out, const da_head_strides& os, cudaStream_t s);
 
-// linear_i8_simt.cu: out[m, n] at (m / tokens) * out_batch + (n / d) * out_head + (m % tokens) * out_token + n % d
+// linear_i8_bytes.cu: rows of any alignment; out[m, n] at (m / tokens) * out_batch + (n / d) * out_head + (m % tokens) * out_token + n % d
 struct LinearArgs {
   const int8_t* x;
   const int8_t* w;
@@ -91,7 +91,7 @@ struct LinearArgs {
   int N, K, d, tokens;
   long long x_stride, w_stride, out_batch, out_head, out_token;
 };
-cudaError_t launch_linear_i8_simt(bool bf16, const LinearArgs& a, cudaStream_t s);
+cudaError_t launch_linear_i8_bytes(bool bf16, const LinearArgs& a, int* status, cudaStream_t s);
 
 // linear_i8_rows.cu: few rows of x; needs linear_i8_tc_supported's alignment too
 bool linear_i8_rows_supported(const LinearArgs& a);

@@ -27,6 +27,7 @@
 // 36 us, 512: 15 us, 128: 10 us.  32760 x 1536 x 1536 60 us (2.55e15): at shallow depths the epilogue is what bounds.
 #include "da_common.cuh"
 #include "da_internal.h"
+#include "linear_i8.cuh"
 #include "tma_host.h"
 
 namespace da {
@@ -38,7 +39,6 @@ constexpr int kTileM = 128;                  // rows of x per CTA
 constexpr int kEpilogueWarps = 8;
 constexpr int kThreads = 128 + 32 * kEpilogueWarps;
 constexpr int kABytes = kTileM * kBlockK;    // 16 KB
-constexpr int kGroupM = 8;                   // row tiles that are walked together for each column tile
 
 constexpr int kMaxN = 256;                   // columns of a tile
 constexpr int kMaxStages = 16;
@@ -97,12 +97,6 @@ __device__ __forceinline__ void arrive_at(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 
-// One lane of a converged warp.
-__device__ __forceinline__ bool elect_one() {
-  uint32_t r;
-  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
-  return r != 0;
-}
 // mbar_wait by a whole warp, with one answer for all lanes.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort, int* status) {
   return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort, status));
@@ -125,20 +119,6 @@ __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map
                  : "memory");
 }
 
-// D (+)= A B^T, signed 8-bit operands from shared memory, 32-bit integer sums
-template <bool kPair>
-__device__ __forceinline__ void mma_i8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
-  if (kPair)
-    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-                 "tcgen05.mma.cta_group::2.kind::i8 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-                 "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
-                 : "memory");
-  else
-    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-                 "tcgen05.mma.cta_group::1.kind::i8 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-                 "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
-                 : "memory");
-}
 // Arrive on `bar` (in both CTAs of a pair) when the products issued so far are done.
 template <bool kPair>
 __device__ __forceinline__ void mma_commit(uint64_t* bar) {
@@ -166,21 +146,6 @@ __device__ __forceinline__ void free_columns(uint32_t t, uint32_t n) {
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(t), "r"(n) : "memory");
   else
     tmem_dealloc(t, n);
-}
-
-// Instruction descriptor: 32-bit integer result, signed 8-bit operands, both K-major.
-__host__ __device__ constexpr uint32_t idesc_i8(int M, int N) {
-  return (2u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
-}
-
-// Tile t of the walk: groups of kGroupM row tiles, column by column, so that the rows of x and w that the
-// resident CTAs read at one time stay in L2.
-__device__ __forceinline__ void tile_at(int t, const Params& p, int& tm, int& tn) {
-  const int per_group = kGroupM * p.tiles_n;
-  const int g = t / per_group, r = t - g * per_group;
-  const int rows = min(kGroupM, p.tiles_m - g * kGroupM);
-  tn = r / rows;
-  tm = g * kGroupM + r - tn * rows;
 }
 
 __device__ __forceinline__ void epilogue_barrier() { asm volatile("bar.sync 1, %0;" ::"n"(32 * kEpilogueWarps) : "memory"); }
@@ -242,7 +207,7 @@ linear_i8_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_const
     bool ok = true;
     for (int t = first; t < tiles && ok; t += step) {
       int tm, tn;
-      tile_at(t, p, tm, tn);
+      tile_at(t, p.tiles_m, p.tiles_n, tm, tn);
       const int row = tm * kRowsPerTile + (int)rank * kTileM;
       const int col = tn * p.n + (int)rank * p.b_rows;
       for (int kb = 0; kb < p.k_blocks; kb += kSub, ++it, turn.next(stages)) {
@@ -323,7 +288,7 @@ linear_i8_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_const
     auto load_scales = [&](int t) {
       if (t >= tiles) return;
       int tm, tn;
-      tile_at(t, p, tm, tn);
+      tile_at(t, p.tiles_m, p.tiles_n, tm, tn);
       const int c = tn * p.n + mine;
       const long long m = (long long)tm * kRowsPerTile + (int)rank * kTileM + ew * 32 + lane;
       const bool in = mine < p.n && c < A.N;
@@ -334,7 +299,7 @@ linear_i8_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_const
     load_scales(first);
     for (int t = first; t < tiles; t += step, ++n) {
       int tm, tn;
-      tile_at(t, p, tm, tn);
+      tile_at(t, p.tiles_m, p.tiles_n, tm, tn);
       const int b = n & 1;
       const int n0 = tn * p.n, n1 = min(n0 + p.n, A.N);   // the tile's columns
       float* cs = s_cols + b * 2 * kMaxN;

@@ -175,12 +175,15 @@ __device__ __forceinline__ void exact_t(const RowArgs& a, const T* x, const T* r
 // The blocks of an SM that a form is compiled for (0: the compiler's choice): their registers bound the warps that hide the
 // loads. The codes of the norm hold the most: rows of 1536 in warps, 129 us with 96 registers, 139 with the 110 of the free
 // choice; rows of 5120 in blocks, 503 us with 80, 516 with 96. The short rows are not held to it (96 wide: 29 us, 34 held).
-template <int MODE, int MAX_THREADS, int ELEMENTS>
-constexpr int kBlocks = MODE != kNormI8 ? 0 : MAX_THREADS == 128 ? (ELEMENTS >= 48 ? 5 : 0) : MAX_THREADS == 256 ? 3 : 0;
+template <int V, int VPT, int MODE, int MAX_THREADS>
+constexpr int kBlocks = MODE != kNormI8 || V == 1 ? 0
+                        : MAX_THREADS == 128 ? (VPT * V >= 48 ? 5 : 0)
+                        : MAX_THREADS == 256 ? 3
+                                             : 0;
 
 // A warp (blocks of 128 threads) or the whole block owns a row; each of its threads holds VPT vectors of V elements.
 template <typename T, int V, int VPT, int MODE, int MAX_THREADS>
-__global__ void __launch_bounds__(MAX_THREADS, (kBlocks<MODE, MAX_THREADS, VPT * V>))
+__global__ void __launch_bounds__(MAX_THREADS, (kBlocks<V, VPT, MODE, MAX_THREADS>))
 row_kernel(const RowArgs a) {
   constexpr bool WARP_ROW = MAX_THREADS == 128;
   using P = Pack<T, V>;
@@ -506,8 +509,13 @@ void launch_block_rows(RowArgs a, unsigned batch, int nvec, cudaStream_t s) {
   const int threads = ((nvec + VPT - 1) / VPT + 31) / 32 * 32;
   a.x_step = vector_step(a, threads * V);
   const dim3 grid((unsigned)a.tokens, batch);
-  if (threads <= 256) row_kernel<T, V, VPT, MODE, 256><<<grid, threads, 0, s>>>(a);
-  else row_kernel<T, V, VPT, MODE, 512><<<grid, threads, 0, s>>>(a);
+  if constexpr (VPT != 8) {   // rows that take 8 vectors a thread fill more than 256 threads
+    if (threads <= 256) {
+      row_kernel<T, V, VPT, MODE, 256><<<grid, threads, 0, s>>>(a);
+      return;
+    }
+  }
+  row_kernel<T, V, VPT, MODE, 512><<<grid, threads, 0, s>>>(a);
 }
 
 // A row of up to 256 vectors is a warp's, so that it needs no barrier; longer ones take the block that holds them with

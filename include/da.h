@@ -337,7 +337,7 @@ DA_API da_status da_rms_norm(int64_t rows, int width, da_dtype dtype, const void
  * so that q * scale is the norm's output to half a step.  q is taken from the exact quotient (fp64
  * where fp32 cannot tell the two sides of a border apart).  A row of zeros gives q = 0, scale = 0; a row with an
  * infinity or NaN (or whose t leaves fp32's range) gives q = 0, scale = NaN, so that products of it
- * are NaN.  q: [rows, width] int8, q_stride elements apart (a multiple of 16 for da_linear_i8's tensor-core path); bytes
+ * are NaN.  q: [rows, width] int8, q_stride elements apart (a multiple of 16 suits da_linear_i8); bytes
  * between width and q_stride are left as they were.  scale: [rows] fp32.  Other arguments and errors as in da_rms_norm,
  * but q and scale share memory with nothing.
  */
@@ -365,9 +365,9 @@ DA_API da_status da_quantize_i8(int B, int H, int N, int d, da_dtype dtype, cons
  * result is rounded once to out_dtype.  x: [B*N, K] int8, w: [H*d, K] int8, rows their strides
  * apart; x_scale: [B*N], w_scale: [H*d], bias: [H*d] (NULL: none), fp32; out: [B,H,N,d] with the
  * given strides, so that V is written as the attention reads it; a plain matrix [M, C] is B = 1,
- * N = M, H = 1, d = C.  H * d < 2^22.  Codes are taken as they are, -128 included.
- * Where x and w and their strides are multiples of 16 bytes the product runs on the tensor cores,
- * otherwise on the CUDA cores.  ws: device workspace of at least 256 bytes, 16-byte aligned,
+ * N = M, H = 1, d = C.  H * d <= 2^22 - 64.  Codes are taken as they are, -128 included.
+ * Rows that start on 16 bytes (x, w and their strides) take tile loads; others cost about five
+ * times as much in large products.  ws: device workspace of at least 256 bytes, 16-byte aligned,
  * zero-filled once (one of da_workspace_bytes serves too): its status word takes a bounded wait
  * that gave up (DA_ERR_TIMEOUT from da_device_status).
  */

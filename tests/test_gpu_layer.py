@@ -360,6 +360,35 @@ def test_linear_over_many_tiles(M, C, K, dtype):
         assert torch.equal(heads.permute(0, 2, 1, 3).reshape(M, C), out[:M, :C])
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("M,C,K,dx,dw", [(1, 40, 3, 1, 2), (130, 200, 125, 3, 0), (129, 129, 129, 1, 1), (300, 1000, 260, 2, 3), (70, 2100, 393, 0, 1),
+                                         (2600, 1300, 1001, 3, 2), (4, 5000, 1536, 1, 0), (33, 32, 128, 2, 2)])
+def test_linear_rows_off_16_bytes(M, C, K, dx, dw, dtype):
+    """Rows that start anywhere: odd strides, odd bases, codes of neighbouring bytes that are not the rows'; heads on the last."""
+    def place(rows, offset, seed):
+        flat = torch.randint(-128, 128, (rows * (K + 5) + 8,), generator=_gen(seed), dtype=torch.int8).cuda()
+        return flat[offset:].as_strided((rows, K), (K + 5, 1))
+    x, w = place(M, dx, 1), place(C, dw, 2)
+    sx, sw, bias = _scales(M, 3), _scales(C, 4), torch.randn(C, generator=_gen(6))
+    ws = torch.zeros(256, dtype=torch.uint8, device="cuda")
+    out = torch.full((M + 1, C + 3), 7.0, dtype=dtype, device="cuda")
+    da.da_linear_i8(x, sx.cuda(), w, sw.cuda(), out[:M, :C], ws, bias=bias.cuda())
+    assert da.da_device_status(ws) == 0
+    _linear_close(out[:M, :C], x.contiguous(), sx, w.contiguous(), sw, bias, dtype)
+    assert (out[M:] == 7).all() and (out[:, C:] == 7).all()
+    aligned = torch.empty_like(out)
+    pad = lambda t: torch.nn.functional.pad(t, (0, -t.shape[1] % 16))[:, :K]           # the same codes in rows of 16 bytes
+    da.da_linear_i8(pad(x), sx.cuda(), pad(w), sw.cuda(), aligned[:M, :C], ws, bias=bias.cuda())
+    assert torch.equal(aligned[:M, :C], out[:M, :C])                 # sums are exact and the epilogues' operations the same
+    if M % 2 == 0 and C % 4 == 0:
+        heads = torch.full((2, 5, M // 2, C // 4), 7.0, dtype=dtype, device="cuda")
+        da.da_linear_i8(x, sx.cuda(), w, sw.cuda(), heads[:, :4], ws, bias=bias.cuda())
+        assert torch.equal(heads[:, :4].permute(0, 2, 1, 3).reshape(M, C), out[:M, :C]) and (heads[:, 4] == 7).all()
+    same = x[:1].expand(M, K)                                        # one row for every token
+    da.da_linear_i8(same, sx.cuda(), w, sw.cuda(), out[:M, :C], ws)
+    _linear_close(out[:M, :C], same.contiguous(), sx, w.contiguous(), sw, None, dtype)
+
+
 def test_linear_extremes():
     """The largest sums (every code -128 at the deepest product), codes of a row that was not finite, zero scales."""
     K = 131071

@@ -9,10 +9,13 @@
 //              swizzle; rows and depth beyond the matrices read as zero);
 //   warp 1     lane 0 issues the products of a stage (four k = 32 steps) into one of two accumulators;
 //   warp 2     allocates tensor memory;
-//   warps 4-11 epilogue: accumulator -> scaled rows -> shared memory -> 16-byte stores of row segments
-//              (the matrix, or the attention's heads: the segment's address is formed from its token and
-//              head), while the next tile's products fill the other accumulator.  Two groups of four warps take
-//              alternate parts of 32 columns: one group alone was the bound at shallow depths.
+//   warps 4-11 epilogue: accumulator -> scaled rows -> shared memory -> the output (the matrix, or the attention's
+//              heads), while the next tile's products fill the other accumulator.  Two groups of four warps take alternate
+//              parts of 32 columns (one was the bound at shallow depths, a third gained nothing).  Boxes of 32 rows x 64 bytes
+//              leave by TMA where the output's strides and widths are multiples of 16 bytes (16000 x 2048 x 512, fp32 out,
+//              43.5 -> 35 us, and 32760 x 1536 x 1536, bf16, 62 -> 59 us against 16-byte stores by the warps); rows on 16
+//              bytes that are no such boxes by 16-byte stores; others element by element, neighbouring lanes neighbouring
+//              columns (16000 x 2049 x 512, fp32, 54 us; 90 with every row's address fetched from the lane that holds it).
 //
 // Two forms.  Pair (kPair): two CTAs of a cluster form a 256 x n tile (n 160 to 256) with cta_group::2; each loads its
 // own 128 rows of x and half of the w rows, so every loaded byte serves 256 rows or n columns.  Single: one CTA forms 128 x n,
@@ -24,7 +27,7 @@
 //
 // Measured, bf16 out: 75600 x 5120 x 5120 1.22 ms cold and 1.31-1.39 ms in a long run under the power cap (3.24e15 and
 // 2.85-3.0e15 op/s; twice the bf16 library rate is 3.38e15 and 2.87e15), the tensor pipe 94 % busy; 2048 x 5120 x 5120
-// 36 us, 512: 15 us, 128: 10 us.  32760 x 1536 x 1536 60 us (2.55e15): at shallow depths the epilogue is what bounds.
+// 36 us, 512: 15 us, 128: 10 us.  32760 x 1536 x 1536 59-61 us (2.6e15): at shallow depths the epilogue is what bounds.
 #include "da_common.cuh"
 #include "da_internal.h"
 #include "linear_i8.cuh"
@@ -36,14 +39,15 @@ namespace {
 
 constexpr int kBlockK = 128;                 // bytes (= elements) of depth per stage
 constexpr int kTileM = 128;                  // rows of x per CTA
-constexpr int kEpilogueWarps = 8;
+constexpr int kEpilogueGroups = 2;            // of four warps
+constexpr int kEpilogueWarps = 4 * kEpilogueGroups;
 constexpr int kThreads = 128 + 32 * kEpilogueWarps;
 constexpr int kABytes = kTileM * kBlockK;    // 16 KB
 
 constexpr int kMaxN = 256;                   // columns of a tile
 constexpr int kMaxStages = 16;
 constexpr int kRingBytes = 6 * 32768;        // the pair's stages at n = 256; a single CTA's 128 + 256 rows fit four times
-constexpr int kStagingBytes = kEpilogueWarps * 2048;   // 32 rows of 64 bytes a warp; behind the ring, and at least the 16 KB that a short tile of x is read beyond it
+constexpr int kStagingBytes = kEpilogueWarps * 2048;   // 32 rows of 64 bytes a warp; behind the ring: a short tile of x is read up to 16 KB beyond it
 constexpr size_t kSmem = 1024 + kRingBytes + kStagingBytes + 2 * 2 * kMaxN * 4 /*scales, bias*/;
 static_assert(kStagingBytes >= kABytes, "a short tile of x is read as a whole one");
 static_assert(kSmem + 1024 <= 232448, "shared memory of one CTA per SM");
@@ -55,6 +59,8 @@ struct Params {
   int a_rows, b_rows; // rows of x and w that a CTA loads for a tile
   int stages;         // of the ring
   int vec;            // rows of the output can be stored 16 bytes at a time
+  int even;           // the 32 rows of a warp are out_token apart
+  int boxes;          // and as boxes of 32 rows x 64 bytes, by TMA
   int* status;
 };
 
@@ -119,6 +125,17 @@ __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map
                  : "memory");
 }
 
+// A box of shared memory into the output; out-of-range rows and columns are not written.
+__device__ __forceinline__ void tma_store_4d(const CUtensorMap* map, uint32_t src, int x, int y, int z, int w) {
+  asm volatile("cp.async.bulk.tensor.4d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4, %5}], [%1];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(src), "r"(x), "r"(y), "r"(z), "r"(w)
+               : "memory");
+  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+// Until this thread's stores have read their shared memory.
+__device__ __forceinline__ void tma_store_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+
 // Arrive on `bar` (in both CTAs of a pair) when the products issued so far are done.
 template <bool kPair>
 __device__ __forceinline__ void mma_commit(uint64_t* bar) {
@@ -153,7 +170,7 @@ __device__ __forceinline__ void epilogue_barrier() { asm volatile("bar.sync 1, %
 template <typename T, bool kPair, int kSub>
 __global__ void __launch_bounds__(kThreads, 1)
 linear_i8_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w,
-                    const __grid_constant__ Params p) {
+                    const __grid_constant__ CUtensorMap tm_out, const __grid_constant__ Params p) {
   extern __shared__ uint8_t smem_raw[];
   __shared__ Bars bars;
   const uint32_t raw = smem_u32(smem_raw);
@@ -273,7 +290,7 @@ linear_i8_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_const
       mbar_wait_drain(&bars.drain, 0);
     }
   } else if (warp >= 4) {
-    const int ew = warp & 3, half = (warp - 4) >> 2;   // rows ew * 32 .. + 32; parts half, half + 2, ...
+    const int ew = warp & 3, group = (warp - 4) >> 2;   // rows ew * 32 .. + 32; parts group, group + kEpilogueGroups, ...
     uint8_t* stage = staging + (warp - 4) * 2048;
     const LinearArgs& A = p.a;
     constexpr int kV = 16 / (int)sizeof(T);          // elements of a 16-byte store
@@ -282,7 +299,7 @@ linear_i8_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_const
     int n = 0;
     bool ok = true;   // after a wait that gave up the loop still runs, so that the warps' barriers match
     // scales and bias of a tile: thread i of the epilogue holds column i's, and its row's scale; loaded a tile ahead
-    static_assert(32 * kEpilogueWarps == kMaxN, "a thread a column");
+    static_assert(32 * kEpilogueWarps >= kMaxN, "a thread a column");
     const int mine = threadIdx.x - 128;
     float col_scale = 0.f, col_bias = 0.f, row_scale = 0.f;
     auto load_scales = [&](int t) {
@@ -303,14 +320,19 @@ linear_i8_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_const
       const int b = n & 1;
       const int n0 = tn * p.n, n1 = min(n0 + p.n, A.N);   // the tile's columns
       float* cs = s_cols + b * 2 * kMaxN;
-      cs[mine] = col_scale;
-      cs[kMaxN + mine] = col_bias;
+      if (mine < kMaxN) {
+        cs[mine] = col_scale;
+        cs[kMaxN + mine] = col_bias;
+      }
       const float sx = row_scale;
       load_scales(t + step);
       const long long m = (long long)tm * kRowsPerTile + (int)rank * kTileM + ew * 32 + lane;
       const int mb = (int)m / A.tokens;   // M stays below 2^31
       const long long off = mb * A.out_batch + ((int)m - mb * A.tokens) * A.out_token;
       const int valid = (int)min(32LL, max(0LL, A.M - (m - lane)));   // rows of this warp inside the matrix
+      long long quad_off[4];   // of the rows whose segments this lane stores
+#pragma unroll
+      for (int i = 0; i < 4; ++i) quad_off[i] = __shfl_sync(0xffffffffu, off, i * 8 + (lane >> 2));
       epilogue_barrier();
       ok = __all_sync(0xffffffffu, ok && mbar_wait(&bars.acc_full[b], (n >> 1) & 1, abort, p.status));
       if (!ok) continue;
@@ -319,12 +341,12 @@ linear_i8_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_const
       // waited for in the turn that asked for it
       const uint32_t acc = tmem + ((uint32_t)(ew * 32) << 16) + b * kMaxN;
       uint32_t r[32];
-      if (n0 + 32 * half < n1) {
-        tmem_ld32(acc + 32 * half, r);
+      if (n0 + 32 * group < n1) {
+        tmem_ld32(acc + 32 * group, r);
         tmem_wait_ld_into(r);
       }
 #pragma unroll 1
-      for (int c0 = 32 * half; n0 + c0 < n1; c0 += 64) {
+      for (int c0 = 32 * group; n0 + c0 < n1; c0 += 32 * kEpilogueGroups) {
         const ulonglong2* sw2 = reinterpret_cast<const ulonglong2*>(cs + c0);
         const ulonglong2* bi2 = reinterpret_cast<const ulonglong2*>(cs + kMaxN + c0);
         const uint64_t sx2 = f2_pack(sx, sx);
@@ -337,11 +359,15 @@ linear_i8_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_const
           f2_unpack(f2_fma(f2_mul(lo, sx2), w.x, bi.x), v[4 * i], v[4 * i + 1]);
           f2_unpack(f2_fma(f2_mul(hi, sx2), w.y, bi.y), v[4 * i + 2], v[4 * i + 3]);
         }
-        const bool more = n0 + c0 + 64 < n1;
-        if (more) tmem_ld32(acc + c0 + 64, r);
+        const bool more = n0 + c0 + 32 * kEpilogueGroups < n1;
+        if (more) tmem_ld32(acc + c0 + 32 * kEpilogueGroups, r);
 #pragma unroll
         for (int g = 0; g < 32 / kSeg; ++g) {   // a segment of 64 bytes a row
-          // row `lane`, 16-byte chunk j at chunk j ^ (row / 2 & 3): neither side of the transposition conflicts
+          if (p.boxes) {   // the store of the segment before has read the staging
+            if (lane == 0) tma_store_read();
+            __syncwarp();
+          }
+          // row `lane`, 16-byte chunk j at chunk j ^ (row / 2 & 3), the 64-byte swizzle: neither side of the transposition conflicts
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             const float* e = v + g * kSeg + j * kV;
@@ -352,8 +378,17 @@ linear_i8_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_const
               o = make_uint4(__float_as_uint(e[0]), __float_as_uint(e[1]), __float_as_uint(e[2]), __float_as_uint(e[3]));
             *reinterpret_cast<uint4*>(stage + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4)) = o;
           }
-          __syncwarp();
           const int s0 = n0 + c0 + g * kSeg;   // the segment's first column
+          if (p.boxes) {
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0 && valid > 0 && s0 < n1) {
+              const int h = s0 / A.d;
+              tma_store_4d(&tm_out, smem_u32(stage), s0 - h * A.d, (int)m - mb * A.tokens, h, mb);
+            }
+            continue;
+          }
+          __syncwarp();
           if (p.vec) {
             // 4 lanes per row segment, 8 rows at a time
             const int c = s0 + (lane & 3) * kV, h = c / A.d;
@@ -361,9 +396,8 @@ linear_i8_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_const
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               const int row = i * 8 + (lane >> 2);
-              const long long ro = __shfl_sync(0xffffffffu, off, row);
               const uint4 o = *reinterpret_cast<const uint4*>(stage + row * 64 + (((lane & 3) ^ ((row >> 1) & 3)) << 4));
-              T* to = static_cast<T*>(A.out) + ro + head;
+              T* to = static_cast<T*>(A.out) + quad_off[i] + head;
               if (row < valid && c < n1) {
                 if (c + kV <= n1) {
                   *reinterpret_cast<uint4*>(to) = o;
@@ -378,16 +412,17 @@ linear_i8_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_const
           } else {
             // rows of any alignment: kSeg lanes a row, neighbouring lanes neighbouring columns
             constexpr int kRows = 32 / kSeg;
-            const int col = lane % kSeg, c = s0 + col, h = c / A.d;
-            const long long head = h * A.out_head + (c - h * A.d);
-            const int byte = col * (int)sizeof(T);
-#pragma unroll 8
+            const int col = lane % kSeg, c = s0 + col, h = c / A.d, first = lane / kSeg;
+            const int byte = col * (int)sizeof(T), below = c < n1 ? valid : 0;
+            T* to = static_cast<T*>(A.out) + (h * A.out_head + (c - h * A.d));
+            if (p.even) to += __shfl_sync(0xffffffffu, off, first);
+#pragma unroll
             for (int i = 0; i < 32; i += kRows) {
-              const int row = i + lane / kSeg;
-              const long long ro = __shfl_sync(0xffffffffu, off, row);
-              if (row < valid && c < n1)
-                static_cast<T*>(A.out)[ro + head] =
-                    *reinterpret_cast<const T*>(stage + row * 64 + (((byte >> 4) ^ ((row >> 1) & 3)) << 4) + (byte & 15));
+              const int row = i + first;
+              T* at = p.even ? to : to + __shfl_sync(0xffffffffu, off, row);
+              // kRows divides 2, so that row / 2 is i / 2
+              if (row < below) *at = *reinterpret_cast<const T*>(stage + row * 64 + (((byte >> 4) ^ ((i >> 1) & 3)) << 4) + (byte & 15));
+              if (p.even) to += kRows * A.out_token;
             }
           }
           __syncwarp();
@@ -401,6 +436,7 @@ linear_i8_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_const
         else mbar_arrive(&bars.acc_empty[b]);
       }
     }
+    if (p.boxes && lane == 0) tma_store_read();   // before the block's memory goes
   }
   __syncwarp();
   tc_fence_before();
@@ -424,15 +460,36 @@ bool make_tmap_i8(CUtensorMap* m, const void* ptr, uint64_t K, uint64_t rows, ui
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// The output as [B][H][tokens][d], stored in boxes of 32 tokens x 64 bytes.
+template <typename T>
+bool make_tmap_out(CUtensorMap* m, const LinearArgs& a) {
+  EncodeTiledFn fn = get_encode_tiled();
+  if (!fn) return false;
+  const cuuint64_t B = a.M / a.tokens, H = a.N / a.d, esz = sizeof(T), row = ((cuuint64_t)a.d * esz + 15) / 16 * 16;
+  // a dimension of one has a stride that nothing uses
+  cuuint64_t dims[4] = {(cuuint64_t)a.d, (cuuint64_t)a.tokens, H, B};
+  cuuint64_t strides[3] = {a.tokens > 1 ? a.out_token * esz : row, H > 1 ? a.out_head * esz : row, B > 1 ? a.out_batch * esz : row};
+  cuuint32_t box[4] = {64 / (cuuint32_t)esz, 32, 1, 1};
+  cuuint32_t estr[4] = {1, 1, 1, 1};
+  return fn(m, sizeof(T) == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, a.out, dims, strides, box,
+            estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <typename T, bool kPair, int kSub>
 cudaError_t launch_sub(const LinearArgs& a, Params& p, int sms, cudaStream_t s) {
   const int stage = kSub * (p.a_rows + p.b_rows) * kBlockK;
   p.stages = kRingBytes / stage < kMaxStages ? kRingBytes / stage : kMaxStages;
   // rows are at least their depth apart (the dispatch sees to it), one row may have any stride
   const uint64_t xs = a.M > 1 ? a.x_stride : (a.K + 15) / 16 * 16, ws = a.N > 1 ? a.w_stride : (a.K + 15) / 16 * 16;
-  CUtensorMap tx, tw;
+  CUtensorMap tx, tw, to{};
   if (!make_tmap_i8(&tx, a.x, a.K, a.M, xs, p.a_rows)) return cudaErrorInvalidValue;
   if (!make_tmap_i8(&tw, a.w, a.K, a.N, ws, p.b_rows)) return cudaErrorInvalidValue;
+  // a box has the tokens of one batch (even), its columns are one tile's and one head's, and a row's last 16 bytes are written whole
+  constexpr int kSeg = 64 / (int)sizeof(T);
+  p.even = a.tokens == a.M || a.tokens % 32 == 0;
+  p.boxes = p.vec && a.d % (kSeg / 4) == 0 && p.even && (p.n % kSeg == 0 || p.tiles_n == 1) &&
+            (a.d == a.N || a.d % kSeg == 0) && make_tmap_out<T>(&to, a);
   auto kernel = linear_i8_tc_kernel<T, kPair, kSub>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
   if (e != cudaSuccess) return e;
@@ -450,7 +507,7 @@ cudaError_t launch_sub(const LinearArgs& a, Params& p, int sms, cudaStream_t s) 
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, tx, tw, p);
+  return cudaLaunchKernelEx(&cfg, kernel, tx, tw, to, p);
 }
 
 template <typename T, bool kPair>

@@ -389,6 +389,29 @@ def test_linear_rows_off_16_bytes(M, C, K, dx, dw, dtype):
     _linear_close(out[:M, :C], same.contiguous(), sx, w.contiguous(), sw, None, dtype)
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("B,H,N,d,K", [(1, 1, 700, 601, 160), (1, 1, 45, 9, 64), (3, 2, 96, 160, 128), (2, 4, 333, 64, 256), (1, 7, 2600, 96, 128), (40, 3, 32, 48, 64),
+                                       (1, 1, 6000, 1337, 128), (2, 3, 64, 80, 128)])
+def test_linear_rows_stored_in_boxes(B, H, N, d, K, dtype):
+    """Outputs whose rows start on 16 bytes, of any width: what lies between and behind the rows stays as it was."""
+    x, w = _codes(B * N, K, K, 1), _codes(H * d, K, K, 2)
+    sx, sw, bias = _scales(B * N, 3), _scales(H * d, 4), torch.randn(H * d, generator=_gen(6))
+    ws = torch.zeros(256, dtype=torch.uint8, device="cuda")
+    pitch = -(-d // 8) * 8
+    heads = torch.full((B, H + 1, N + 2, pitch), 7.0, dtype=dtype, device="cuda")
+    tokens = torch.full((B, N + 1, H + 1, pitch), 7.0, dtype=dtype, device="cuda")
+    flat = None
+    for base, out in ((heads, heads[:, :H, :N, :d]), (tokens, tokens[:, :N, :H, :d].permute(0, 2, 1, 3))):
+        da.da_linear_i8(x, sx.cuda(), w, sw.cuda(), out, ws, bias=bias.cuda())
+        got = out.permute(0, 2, 1, 3).reshape(B * N, H * d)
+        if flat is None:
+            _linear_close(got, x, sx, w, sw, bias, dtype)
+            flat = got.clone()
+        assert torch.equal(got, flat)
+        out.fill_(7)
+        assert (base == 7).all() and da.da_device_status(ws) == 0
+
+
 def test_linear_extremes():
     """The largest sums (every code -128 at the deepest product), codes of a row that was not finite, zero scales."""
     K = 131071

@@ -21,9 +21,10 @@
 // 338 us against 264 then; norm: 481 against 451): the registers of the loads ahead cost more warps than they hide.
 //
 // Measured, bf16: norm with residual 75600 x 5120 451 us (6.86 TB/s, 1.07 of the plain copy's rate); codes of the norm with
-// residual 75600 x 1536 140 us (5.8 TB/s), x 5120 524 us (5.2 TB/s: two barriers a row, and a third for the 46 % of the
-// rows that need a second look); codes of 40 heads of 75600 tokens 200 us (5.8 TB/s).  Rows whose width or start is odd are
-// walked element by element, at a quarter to a half of these rates.
+// residual 75600 x 1536 129 us (6.3 TB/s), x 5120 503 us (5.4 TB/s: two barriers a row, and a third for the 46 % of the
+// rows that need a second look); codes of 40 heads of 75600 tokens 194 us (6.0 TB/s).  Rows that do not start on 16 bytes are
+// walked in pairs (bf16, even) or element by element: norm with residual 75600 x 1001 185 us in bf16 (0.5 of the copy's
+// rate) and 187 in fp32 (1.0), codes 290 and 261 (0.3 and 0.6).
 #include "da_common.cuh"
 #include "da_internal.h"
 
@@ -102,6 +103,25 @@ struct Pack<float, 4> {
   static __device__ __forceinline__ uint32_t max_float(uint32_t m) { return m; }
 };
 template <>
+struct Pack<__nv_bfloat16, 2> {
+  using Raw = uint32_t;
+  static __device__ __forceinline__ Raw zero() { return 0; }
+  static __device__ __forceinline__ Raw load(const __nv_bfloat16* p) { return *reinterpret_cast<const uint32_t*>(p); }
+  static __device__ __forceinline__ void unpack(Raw r, float* o) {
+    o[0] = __uint_as_float(r << 16);
+    o[1] = __uint_as_float(r & 0xffff0000u);
+  }
+  static __device__ __forceinline__ void store(__nv_bfloat16* p, const float* v) {
+    *reinterpret_cast<uint32_t*>(p) = pack_bf16x2(v[0], v[1]);
+  }
+  static __device__ __forceinline__ void store_codes(int8_t* p, const uint32_t* q) {
+    *reinterpret_cast<uint16_t*>(p) = (uint16_t)__byte_perm(q[0], q[1], 0x0040);
+  }
+  // two maxima side by side, in the halves of a word
+  static __device__ __forceinline__ uint32_t max_bits(uint32_t m, Raw r) { return __vmaxu2(m, r & 0x7fff7fffu); }
+  static __device__ __forceinline__ uint32_t max_float(uint32_t m) { return max(m << 16, m & 0xffff0000u); }
+};
+template <>
 struct Pack<__nv_bfloat16, 8> {
   using Raw = uint4;
   static __device__ __forceinline__ Raw zero() { return make_uint4(0, 0, 0, 0); }
@@ -176,7 +196,7 @@ __device__ __forceinline__ void exact_t(const RowArgs& a, const T* x, const T* r
 // loads. The codes of the norm hold the most: rows of 1536 in warps, 129 us with 96 registers, 139 with the 110 of the free
 // choice; rows of 5120 in blocks, 503 us with 80, 516 with 96. The short rows are not held to it (96 wide: 29 us, 34 held).
 template <int V, int VPT, int MODE, int MAX_THREADS>
-constexpr int kBlocks = MODE != kNormI8 || V == 1 ? 0
+constexpr int kBlocks = MODE != kNormI8 || V <= 2 ? 0
                         : MAX_THREADS == 128 ? (VPT * V >= 48 ? 5 : 0)
                         : MAX_THREADS == 256 ? 3
                                              : 0;
@@ -509,7 +529,7 @@ void launch_block_rows(RowArgs a, unsigned batch, int nvec, cudaStream_t s) {
   const int threads = ((nvec + VPT - 1) / VPT + 31) / 32 * 32;
   a.x_step = vector_step(a, threads * V);
   const dim3 grid((unsigned)a.tokens, batch);
-  if constexpr (VPT != 8) {   // rows that take 8 vectors a thread fill more than 256 threads
+  if constexpr (VPT != 8 && VPT != 16) {   // rows that take 8 or 16 vectors a thread fill more than 256 threads
     if (threads <= 256) {
       row_kernel<T, V, VPT, MODE, 256><<<grid, threads, 0, s>>>(a);
       return;
@@ -524,7 +544,7 @@ template <typename T, int V, int MODE>
 cudaError_t launch_rows_v(const RowArgs& a, cudaStream_t s) {
   const int nvec = (a.width + V - 1) / V;
   const unsigned batch = (unsigned)(a.rows / a.tokens);
-  if constexpr (V > 1) {
+  if constexpr (V > 2) {
     if (nvec <= 32) launch_warp_rows<T, V, 1, MODE>(a, batch, s);
     else if (nvec <= 64) launch_warp_rows<T, V, 2, MODE>(a, batch, s);
     else if (nvec <= 128) launch_warp_rows<T, V, 4, MODE>(a, batch, s);
@@ -534,10 +554,11 @@ cudaError_t launch_rows_v(const RowArgs& a, cudaStream_t s) {
     else if (V < 8 && nvec <= 4096) launch_block_rows<T, V, V < 8 ? 8 : 4, MODE>(a, batch, nvec, s);
     else return cudaErrorInvalidValue;
   } else {
+    constexpr int kLast = V == 2 ? 16 : 32;
     if (nvec <= 128) launch_warp_rows<T, V, 4, MODE>(a, batch, s);
     else if (nvec <= 2048) launch_block_rows<T, V, 4, MODE>(a, batch, nvec, s);
     else if (nvec <= 4096) launch_block_rows<T, V, 8, MODE>(a, batch, nvec, s);
-    else if (nvec <= 16384) launch_block_rows<T, V, 32, MODE>(a, batch, nvec, s);
+    else if (nvec <= 512 * kLast) launch_block_rows<T, V, kLast, MODE>(a, batch, nvec, s);
     else return cudaErrorInvalidValue;
   }
   return cudaGetLastError();
@@ -545,24 +566,29 @@ cudaError_t launch_rows_v(const RowArgs& a, cudaStream_t s) {
 
 bool aligned_for(const void* p, size_t bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
 
-// The vector form needs every row of every tensor to start on the width of its vector.
+// Vectors of V elements need every row of every tensor to start on their width.
 template <typename T, int V, int MODE>
-cudaError_t launch_rows_t(const RowArgs& a, cudaStream_t s) {
+bool rows_fit(const RowArgs& a) {
   const size_t in = sizeof(T) * V, out = MODE == kNorm ? in : (size_t)V;
   bool vec = a.width % V == 0 && a.head_dim % V == 0 && aligned_for(a.x, in) && a.x_batch % V == 0 &&
              a.x_head % V == 0 && a.x_token % V == 0 && aligned_for(a.out, out) && a.out_stride % V == 0;
   if (a.residual) vec = vec && aligned_for(a.residual, in) && a.r_stride % V == 0;
   if (a.sum_out) vec = vec && aligned_for(a.sum_out, in) && a.sum_stride % V == 0;
   if (a.weight) vec = vec && aligned_for(a.weight, in);
-  return vec ? launch_rows_v<T, V, MODE>(a, s) : launch_rows_v<T, 1, MODE>(a, s);
+  return vec;
 }
 
 // The reciprocal that x_offset multiplies by; a head of one element needs none (2^32 does not fit).
 uint32_t per_head(int d) { return d == 1 ? 0u : (uint32_t)(((1ull << 32) + d - 1) / d); }
 
+// 16 bytes of a row a load, or the elements one by one (4 bytes in fp32).  In bf16 pairs come between: 37000 rows of 1002,
+// norm 37 us and 66 one by one, codes 76 and 142; of 9002, 383 and 1020, 668 and 1650.
 template <int MODE>
 cudaError_t launch_rows(bool bf16, const RowArgs& a, cudaStream_t s) {
-  return bf16 ? launch_rows_t<__nv_bfloat16, 8, MODE>(a, s) : launch_rows_t<float, 4, MODE>(a, s);
+  using B = __nv_bfloat16;
+  if (!bf16) return rows_fit<float, 4, MODE>(a) ? launch_rows_v<float, 4, MODE>(a, s) : launch_rows_v<float, 1, MODE>(a, s);
+  if (rows_fit<B, 8, MODE>(a)) return launch_rows_v<B, 8, MODE>(a, s);
+  return rows_fit<B, 2, MODE>(a) ? launch_rows_v<B, 2, MODE>(a, s) : launch_rows_v<B, 1, MODE>(a, s);
 }
 
 }  // namespace

@@ -52,7 +52,7 @@ def _norm_close(got, ref, dtype):
 # ---------------------------------------------------------------------------
 # norm and its codes
 
-WIDTHS = [1, 7, 8, 64, 97, 128, 255, 257, 512, 1000, 1001, 1024, 1536, 2056, 4100, 5120, 8192, 16380, 16383, 16384]
+WIDTHS = [1, 2, 7, 8, 64, 97, 128, 130, 255, 257, 258, 512, 1000, 1001, 1002, 1024, 1536, 2056, 2132, 4098, 4100, 5120, 8192, 8198, 16380, 16382, 16383, 16384]
 
 
 def _rows_case(rows, width, dtype, residual, seed):
@@ -271,7 +271,7 @@ def test_strides_of_single_entries_do_not_matter():
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
-@pytest.mark.parametrize("B,H,N,d", [(1, 1, 1, 64), (2, 3, 37, 64), (1, 12, 130, 128), (3, 40, 5, 128), (2, 5, 19, 24), (1, 7, 3, 9)])
+@pytest.mark.parametrize("B,H,N,d", [(1, 1, 1, 64), (2, 3, 37, 64), (1, 12, 130, 128), (3, 40, 5, 128), (2, 5, 19, 24), (1, 7, 3, 9), (2, 3, 31, 10), (1, 40, 6, 50), (1, 100, 3, 90)])
 def test_quantize_heads(B, H, N, d, dtype):
     x = (torch.randn(B, H, N, d, generator=_gen(B + N)) * 3).to(dtype)
     ref, m = oracle.row_codes(x.permute(0, 2, 1, 3).reshape(B * N, H * d))

@@ -7,9 +7,9 @@
 // together and writes them where the 128-byte swizzle puts them.  A CTA forms 128 x n outputs (n = 128, or 64 or 32 where that
 // fills the GPU) from slices of 128 deep in two buffers: a slice's words are loaded into registers while the one before is
 // multiplied.  Two CTAs an SM.  The loads bound it, by their latency where there are few tiles and by their number where there
-// are many.  Measured, bf16 out: 777 x 1537 x 1001 22 us, 2048 x 5120 x 5121 243 us, 8192 x 5120 x 5121 840 us (5.1e14 op/s, a
+// are many.  Measured, bf16 out: 777 x 1537 x 1001 19 us, 2048 x 5120 x 5121 209 us, 8192 x 5120 x 5121 722 us (5.9e14 op/s, a
 // fifth of the rate of rows on 16 bytes; four products an instruction on the CUDA cores reached 8e13).  Taking a thread's second
-// word from its neighbour by shuffles halves the loads and was slower (950 us).  The quantisers write rows that need none of it.
+// word from its neighbour by shuffles halves the loads and was slower (950 us against 840 then).  The quantisers write rows that need none of it.
 #include "da_common.cuh"
 #include "da_internal.h"
 #include "linear_i8.cuh"
@@ -37,18 +37,25 @@ __device__ __forceinline__ uint2 bytes_within(uintptr_t p, uintptr_t lo, uintptr
   return make_uint2((uint32_t)v, (uint32_t)(v >> 32));
 }
 
-// Rows of x or w that a tile reads, and where their matrix begins and ends.
+// Rows of x or w that a tile reads, as a thread sees them: it takes row `place` of each chunk of 16.  Those rows are
+// 16 strides apart, so they all start at the same place within 8 bytes.
 struct Rows {
-  uintptr_t base, lo, hi;
-  long long stride;
-  int count;
-  __device__ __forceinline__ Rows(const int8_t* matrix, long long of, long long stride_, long long first, int count_, int K)
-      : base(reinterpret_cast<uintptr_t>(matrix + first * stride_)), lo(reinterpret_cast<uintptr_t>(matrix)),
-        hi(reinterpret_cast<uintptr_t>(matrix + (of - 1) * stride_ + K)), stride(stride_), count(count_) {}
+  uintptr_t first, any;   // this thread's first row and a row that is always there, down to a multiple of 8
+  uintptr_t lo, hi;       // where the matrix begins and ends
+  long long step;
+  int count, place, skew;   // rows of the tile; skew: bytes from `first` to the row
+
+  __device__ __forceinline__ Rows(const int8_t* matrix, long long of, long long stride, long long row0, int count_, int place_, int K)
+      : lo(reinterpret_cast<uintptr_t>(matrix)), hi(reinterpret_cast<uintptr_t>(matrix + (of - 1) * stride + K)), step(kChunk * stride),
+        count(count_), place(place_) {
+    const uintptr_t base = lo + (uintptr_t)(row0 * stride), mine = base + (uintptr_t)(place_ * stride);
+    skew = (int)(mine & 7);
+    first = mine - skew;
+    any = base & ~(uintptr_t)7;
+  }
 };
 
-// A thread's part of a slice of kChunks chunks of rows: for row 16 i + its half-warp's place, the two aligned 8 bytes that
-// bytes [k, k + 8) lie in.  Rows beyond the matrix are its last row again.
+// A thread's part of a slice: for its row of every chunk, the two aligned 8 bytes that bytes [k, k + 8) lie in.
 template <int kChunks>
 struct Words {
   uint2 lo[kChunks], hi[kChunks];
@@ -56,33 +63,32 @@ struct Words {
   // kInside: the words around the bytes lie in the row.  Otherwise a word is read where it holds bytes of the row, and where
   // it reaches out of the matrix byte by byte.
   template <bool kInside>
-  __device__ __forceinline__ void load(const Rows& m, int place, int k, int K) {
+  __device__ __forceinline__ void load(const Rows& m, int k, int K) {
+    uintptr_t row = m.first + k;
 #pragma unroll
-    for (int i = 0; i < kChunks; ++i) {
+    for (int i = 0; i < kChunks; ++i, row += m.step) {
       if (i * kChunk >= m.count) break;
-      const uintptr_t row = m.base + (uintptr_t)((long long)min(i * kChunk + place, m.count - 1) * m.stride);
-      const uintptr_t at = (row & ~(uintptr_t)7) + k;
+      const uintptr_t at = i * kChunk + m.place < m.count ? row : m.any + k;
       if (kInside) {
         lo[i] = *reinterpret_cast<const uint2*>(at);
         hi[i] = *reinterpret_cast<const uint2*>(at + 8);
       } else {
         lo[i] = hi[i] = make_uint2(0, 0);
-        if (at < row + K) lo[i] = bytes_within(at, m.lo, m.hi);
-        if (at + 8 < row + K) hi[i] = bytes_within(at + 8, m.lo, m.hi);
+        if (k < K + m.skew) lo[i] = bytes_within(at, m.lo, m.hi);
+        if (k + 8 < K + m.skew) hi[i] = bytes_within(at + 8, m.lo, m.hi);
       }
     }
   }
   // To rows of 128 bytes in the 128-byte swizzle; mask keeps the bytes before the end of a row.
-  __device__ __forceinline__ void store(uint8_t* to, const Rows& m, int place, int l, uint2 mask) const {
+  __device__ __forceinline__ void store(uint8_t* to, const Rows& m, int l, uint2 mask) const {
+    const bool far = m.skew & 4;
+    const uint32_t shift = (m.skew & 3) * 8;
+    uint8_t* at = to + m.place * kBlockK + (((l >> 1) ^ (m.place & 7)) << 4) + (l & 1) * 8;
 #pragma unroll
     for (int i = 0; i < kChunks; ++i) {
       if (i * kChunk >= m.count) break;
-      const uint32_t first = (uint32_t)m.base + (uint32_t)min(i * kChunk + place, m.count - 1) * (uint32_t)m.stride;
-      const bool far = first & 4;
       const uint32_t a = far ? lo[i].y : lo[i].x, b = far ? hi[i].x : lo[i].y, c = far ? hi[i].y : hi[i].x;
-      const uint32_t shift = (first & 3) * 8;
-      const int r = i * kChunk + place;
-      *reinterpret_cast<uint2*>(to + r * kBlockK + (((l >> 1) ^ (r & 7)) << 4) + (l & 1) * 8) =
+      *reinterpret_cast<uint2*>(at + i * kChunk * kBlockK) =
           make_uint2(__funnelshift_r(a, b, shift) & mask.x, __funnelshift_r(b, c, shift) & mask.y);
     }
   }
@@ -123,20 +129,20 @@ linear_i8_bytes_kernel(const LinearArgs a, int tiles_m, int tiles_n, int* status
   tc_fence_after();
   const uint32_t tmem = tmem_base;
 
-  const Rows x(a.x, a.M, a.x_stride, m0, rows, a.K), w(a.w, a.N, a.w_stride, n0, cols, a.K);
-  const int slices = (a.K + kBlockK - 1) / kBlockK;
   const int place = threadIdx.x >> 4, l = threadIdx.x & 15;
+  const Rows x(a.x, a.M, a.x_stride, m0, rows, place, a.K), w(a.w, a.N, a.w_stride, n0, cols, place, a.K);
+  const int slices = (a.K + kBlockK - 1) / kBlockK;
   Words<kXChunks> xw;
   Words<n / kChunk> ww;
   auto load = [&](int kb) {
     const int k0 = kb * kBlockK, k = k0 + 8 * l;
     // between the first and the last slices the words around a thread's bytes lie in its row
     if (k0 > 0 && k0 + kBlockK + 8 <= a.K) {
-      xw.template load<true>(x, place, k, a.K);
-      ww.template load<true>(w, place, k, a.K);
+      xw.template load<true>(x, k, a.K);
+      ww.template load<true>(w, k, a.K);
     } else {
-      xw.template load<false>(x, place, k, a.K);
-      ww.template load<false>(w, place, k, a.K);
+      xw.template load<false>(x, k, a.K);
+      ww.template load<false>(w, k, a.K);
     }
   };
   bool ok = true;
@@ -148,8 +154,8 @@ linear_i8_bytes_kernel(const LinearArgs a, int tiles_m, int tiles_n, int* status
     if (ok) {
       const int left = a.K - kb * kBlockK - 8 * l;
       const uint2 mask = make_uint2(first_bytes(left), first_bytes(left - 4));
-      xw.store(to, x, place, l, mask);
-      ww.store(to + kTileM * kBlockK, w, place, l, mask);
+      xw.store(to, x, l, mask);
+      ww.store(to + kTileM * kBlockK, w, l, mask);
     }
     if (kb + 1 < slices) load(kb + 1);
     fence_async_smem();

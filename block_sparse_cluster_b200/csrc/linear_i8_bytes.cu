@@ -7,9 +7,10 @@
 // together and writes them where the 128-byte swizzle puts them.  A CTA forms 128 x n outputs (n = 128, or 64 or 32 where that
 // fills the GPU) from slices of 128 deep in two buffers: a slice's words are loaded into registers while the one before is
 // multiplied.  Two CTAs an SM.  The loads bound it, by their latency where there are few tiles and by their number where there
-// are many.  Measured, bf16 out: 777 x 1537 x 1001 19 us, 2048 x 5120 x 5121 209 us, 8192 x 5120 x 5121 722 us (5.9e14 op/s, a
-// fifth of the rate of rows on 16 bytes; four products an instruction on the CUDA cores reached 8e13).  Taking a thread's second
-// word from its neighbour by shuffles halves the loads and was slower (950 us against 840 then).  The quantisers write rows that need none of it.
+// are many.  Measured, bf16 out: 777 x 1537 x 1001 18 us, 2048 x 5120 x 5121 173 us, 8192 x 5120 x 5121 607 us (7.1e14 op/s, a
+// quarter of the rate of rows on 16 bytes; four products an instruction on the CUDA cores reached 8e13).  Taking a thread's second
+// word from its neighbour by shuffles halves the loads and was slower (950 us against 840 then); full
+// tiles without a test a chunk are faster (722 -> 607).  The quantisers write rows that need none of it.
 #include "da_common.cuh"
 #include "da_internal.h"
 #include "linear_i8.cuh"
@@ -61,14 +62,14 @@ struct Words {
   uint2 lo[kChunks], hi[kChunks];
 
   // kInside: the words around the bytes lie in the row.  Otherwise a word is read where it holds bytes of the row, and where
-  // it reaches out of the matrix byte by byte.
-  template <bool kInside>
+  // it reaches out of the matrix byte by byte.  kFull: the tile has all its rows.
+  template <bool kInside, bool kFull>
   __device__ __forceinline__ void load(const Rows& m, int k, int K) {
     uintptr_t row = m.first + k;
 #pragma unroll
     for (int i = 0; i < kChunks; ++i, row += m.step) {
-      if (i * kChunk >= m.count) break;
-      const uintptr_t at = i * kChunk + m.place < m.count ? row : m.any + k;
+      if (!kFull && i * kChunk >= m.count) break;
+      const uintptr_t at = kFull || i * kChunk + m.place < m.count ? row : m.any + k;
       if (kInside) {
         lo[i] = *reinterpret_cast<const uint2*>(at);
         hi[i] = *reinterpret_cast<const uint2*>(at + 8);
@@ -79,18 +80,28 @@ struct Words {
       }
     }
   }
+  __device__ __forceinline__ void load(const Rows& m, bool inside, int k, int K) {
+    if (!inside) load<false, false>(m, k, K);
+    else if (m.count == kChunks * kChunk) load<true, true>(m, k, K);
+    else load<true, false>(m, k, K);
+  }
   // To rows of 128 bytes in the 128-byte swizzle; mask keeps the bytes before the end of a row.
+  template <bool kFull>
   __device__ __forceinline__ void store(uint8_t* to, const Rows& m, int l, uint2 mask) const {
     const bool far = m.skew & 4;
     const uint32_t shift = (m.skew & 3) * 8;
     uint8_t* at = to + m.place * kBlockK + (((l >> 1) ^ (m.place & 7)) << 4) + (l & 1) * 8;
 #pragma unroll
     for (int i = 0; i < kChunks; ++i) {
-      if (i * kChunk >= m.count) break;
+      if (!kFull && i * kChunk >= m.count) break;
       const uint32_t a = far ? lo[i].y : lo[i].x, b = far ? hi[i].x : lo[i].y, c = far ? hi[i].y : hi[i].x;
       *reinterpret_cast<uint2*>(at + i * kChunk * kBlockK) =
           make_uint2(__funnelshift_r(a, b, shift) & mask.x, __funnelshift_r(b, c, shift) & mask.y);
     }
+  }
+  __device__ __forceinline__ void put(uint8_t* to, const Rows& m, int l, uint2 mask) const {
+    if (m.count == kChunks * kChunk) store<true>(to, m, l, mask);
+    else store<false>(to, m, l, mask);
   }
 };
 
@@ -137,13 +148,9 @@ linear_i8_bytes_kernel(const LinearArgs a, int tiles_m, int tiles_n, int* status
   auto load = [&](int kb) {
     const int k0 = kb * kBlockK, k = k0 + 8 * l;
     // between the first and the last slices the words around a thread's bytes lie in its row
-    if (k0 > 0 && k0 + kBlockK + 8 <= a.K) {
-      xw.template load<true>(x, k, a.K);
-      ww.template load<true>(w, k, a.K);
-    } else {
-      xw.template load<false>(x, k, a.K);
-      ww.template load<false>(w, k, a.K);
-    }
+    const bool inside = k0 > 0 && k0 + kBlockK + 8 <= a.K;
+    xw.load(x, inside, k, a.K);
+    ww.load(w, inside, k, a.K);
   };
   bool ok = true;
   load(0);
@@ -154,8 +161,8 @@ linear_i8_bytes_kernel(const LinearArgs a, int tiles_m, int tiles_n, int* status
     if (ok) {
       const int left = a.K - kb * kBlockK - 8 * l;
       const uint2 mask = make_uint2(first_bytes(left), first_bytes(left - 4));
-      xw.store(to, x, l, mask);
-      ww.store(to + kTileM * kBlockK, w, l, mask);
+      xw.put(to, x, l, mask);
+      ww.put(to + kTileM * kBlockK, w, l, mask);
     }
     if (kb + 1 < slices) load(kb + 1);
     fence_async_smem();

@@ -367,7 +367,8 @@ DA_API da_status da_quantize_i8(int B, int H, int N, int d, da_dtype dtype, cons
  * given strides, so that V is written as the attention reads it; a plain matrix [M, C] is B = 1,
  * N = M, H = 1, d = C.  H * d <= 2^22 - 64.  Codes are taken as they are, -128 included.
  * Rows that start on 16 bytes (x, w and their strides) take tile loads; others cost about four
- * times as much in large products.  ws: device workspace of at least 256 bytes, 16-byte aligned,
+ * times as much in large products.  Fastest are rows of x and w a multiple of 128 bytes apart and rows of
+ * out a multiple of 32.  ws: device workspace of at least 256 bytes, 16-byte aligned,
  * zero-filled once (one of da_workspace_bytes serves too): its status word takes a bounded wait
  * that gave up (DA_ERR_TIMEOUT from da_device_status).
  */

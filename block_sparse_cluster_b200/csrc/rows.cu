@@ -7,6 +7,8 @@
 //              scale = m / (127 sqrt(mean v^2 + eps));  the norm's own factor cancels in q
 //   quantize:  t = x,  scale = m / 127
 // A row of zeros has scale 0 and codes 0; a row with an infinity or a NaN has scale NaN and codes 0.
+// Where mean v^2 + eps leaves [kLeastMean, fp32's largest number), squares or their sum are no fp32 numbers any more (from
+// about 1e17 on in wide rows, and with eps = 0 from about 1e-15 down): such a row is squared again, times a power of two.
 //
 // Codes are the nearest ones of the exact quotient.  fp32 gives t * (127 / m) to within kNear of it; where that lies
 // so close to a border k + 1/2, the codes of the vector are taken again from the inputs, comparing 127 |t| with
@@ -51,6 +53,9 @@ constexpr float kSplit = 65.f;
 // rounds once, 127 u < 2^-16; the norm's t rounds twice (sum, product) and so does the m taken from it: 5 * 127 u < 2^-14.
 template <int MODE>
 constexpr float kNear = MODE == kQuantI8 ? 1.52587891e-5f : 6.10351562e-5f;
+
+// 2^-100.  A square below fp32's normal numbers is off by up to 2^-150, and so is the mean of them: 2^-50 of this, not seen.
+constexpr float kLeastMean = 0x1p-100f;
 
 __device__ __forceinline__ float max3_nan(float a, float b, float c) {   // a NaN wins over every number
   float r;
@@ -172,12 +177,12 @@ __device__ __forceinline__ long long x_offset(const RowArgs& a, int c) {
   return h * a.x_head + (c - h * a.head_dim);
 }
 
-// t = (x + r) w in fp64 of the V elements from column c on.
+// t = (x + r) w in fp64 of the V elements from column c on, of a norm.
 template <typename T, int V>
-__device__ __forceinline__ void exact_t(const RowArgs& a, const T* x, const T* r, const T* w, int c, double* t) {
+__device__ __forceinline__ void exact_t(const T* x, const T* r, const T* w, int c, double* t) {
   using P = Pack<T, V>;
   float f[V];
-  P::unpack(P::load(x + x_offset(a, c)), f);
+  P::unpack(P::load(x + c), f);
 #pragma unroll
   for (int e = 0; e < V; ++e) t[e] = f[e];
   if (r) {
@@ -192,13 +197,115 @@ __device__ __forceinline__ void exact_t(const RowArgs& a, const T* x, const T* r
   }
 }
 
+// The power of two that brings the row into fp32's range once mean v^2 + eps has left [kLeastMean, infinity).  Above:
+// some |v| >= 2^57 (2^14 columns), and 2^14 (2^(128 - 72))^2 is still a number.  Below: 2^-43 > |v|, whose shifted squares sum to
+// less than 2^114, and the smallest subnormal becomes 2^-49.  A NaN stays one.
+__device__ __forceinline__ float wide_shift(float mean) { return mean < kLeastMean ? 0x1p100f : 0x1p-72f; }
+
+// 1 / sqrt(mean + eps) of the row divided by shift, from a thread's part of the sum of (v shift)^2; in a fixed order.
+// part: the block's scratch, when it owns the row.
+template <bool WARP_ROW>
+__device__ __forceinline__ float wide_root(float squares, float shift, float inv_width, float eps, float* part) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) squares += __shfl_xor_sync(0xffffffffu, squares, o);
+  if (!WARP_ROW) {
+    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = squares;
+    __syncthreads();
+    squares = 0.f;
+#pragma unroll 1
+    for (int i = 0; i < (int)blockDim.x >> 5; ++i) squares += part[i];
+  }
+  return rsqrtf(squares * inv_width + eps * shift * shift);
+}
+
+// The norm's output of a wide row, from the inputs.  A thread reads a vector before it writes it, so that sum and out may be the
+// inputs' buffers.
+template <typename T, int V, bool WARP_ROW>
+__device__ __noinline__ void wide_norm(const T* x, const T* r, const T* w, T* sum, T* out, int first, int width, int step,
+                                       float inv_width, float eps, float mean, float* part) {
+  using P = Pack<T, V>;
+  const float shift = wide_shift(mean);
+  float f[V], g[V], squares = 0.f;
+  auto load_v = [&](int c) {
+    P::unpack(P::load(x + c), f);
+    if (r) {
+      P::unpack(P::load(r + c), g);
+#pragma unroll
+      for (int e = 0; e < V; ++e) f[e] += g[e];
+    }
+  };
+#pragma unroll 1
+  for (int c = first; c < width; c += step) {
+    load_v(c);
+#pragma unroll
+    for (int e = 0; e < V; ++e) squares = fmaf(f[e] * shift, f[e] * shift, squares);
+  }
+  const float root = wide_root<WARP_ROW>(squares, shift, inv_width, eps, part);
+#pragma unroll 1
+  for (int c = first; c < width; c += step) {
+    load_v(c);
+    if (sum) P::store(sum + c, f);
+#pragma unroll
+    for (int e = 0; e < V; ++e) f[e] = f[e] * shift * root;
+    if (w) {
+      P::unpack(P::load(w + c), g);
+#pragma unroll
+      for (int e = 0; e < V; ++e) f[e] *= g[e];
+    }
+    P::store(out + c, f);
+  }
+}
+
+// The norm's codes, scale and sum of a row of which fp32 loses the statistics or the t; as in wide_norm.  top: zero, the
+// block's scratch, when it owns the row.
+template <typename T, int V, bool WARP_ROW>
+__device__ __forceinline__ void wide_codes(const T* x, const T* r, const T* w, T* sum, int8_t* q, float* scale, int first, int width, int step,
+                                        float inv_width, float eps, float shift, float* part, unsigned long long* top) {
+  using P = Pack<T, V>;
+  float squares = 0.f;
+  unsigned long long best = 0;   // bits of max |t|, which order as integers
+#pragma unroll 1
+  for (int c = first; c < width; c += step) {
+    double t[V];
+    exact_t<T, V>(x, r, nullptr, c, t);
+#pragma unroll
+    for (int e = 0; e < V; ++e) squares = fmaf((float)t[e] * shift, (float)t[e] * shift, squares);
+    exact_t<T, V>(x, r, w, c, t);
+#pragma unroll
+    for (int e = 0; e < V; ++e) best = max(best, (unsigned long long)__double_as_longlong(fabs(t[e])));
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) best = max(best, __shfl_xor_sync(0xffffffffu, best, o));
+  if (!WARP_ROW && (threadIdx.x & 31) == 0) atomicMax(top, best);
+  const float root = wide_root<WARP_ROW>(squares, shift, inv_width, eps, part);   // the block's barrier is in it
+  if (!WARP_ROW) best = *top;
+  const double m = __longlong_as_double((long long)best);
+  if (first == 0) *scale = m > 0.0 ? (float)(m * root * shift * (1.0 / 127.0)) : 0.f;
+#pragma unroll 1
+  for (int c = first; c < width; c += step) {
+    double t[V];
+    uint32_t code[V];
+    exact_t<T, V>(x, r, w, c, t);
+#pragma unroll
+    for (int e = 0; e < V; ++e) code[e] = m > 0.0 ? (uint32_t)(int)rint(127.0 * t[e] / m) : 0;
+    P::store_codes(q + c, code);
+    if (sum) {
+      float f[V];
+      exact_t<T, V>(x, r, nullptr, c, t);
+#pragma unroll
+      for (int e = 0; e < V; ++e) f[e] = (float)t[e];
+      P::store(sum + c, f);
+    }
+  }
+}
+
 // The blocks of an SM that a form is compiled for (0: the compiler's choice): their registers bound the warps that hide the
 // loads. The codes of the norm hold the most: rows of 1536 in warps, 129 us with 96 registers, 139 with the 110 of the free
-// choice; rows of 5120 in blocks, 503 us with 80, 516 with 96. The short rows are not held to it (96 wide: 29 us, 34 held).
+// choice; rows of 5120 in blocks, 421 us with 64, 553 with 80. The short rows are not held to it (96 wide: 29 us, 34 held).
 template <int V, int VPT, int MODE, int MAX_THREADS>
 constexpr int kBlocks = MODE != kNormI8 || V <= 2 ? 0
                         : MAX_THREADS == 128 ? (VPT * V >= 48 ? 5 : 0)
-                        : MAX_THREADS == 256 ? 3
+                        : MAX_THREADS == 256 ? 4
                                              : 0;
 
 // A warp (blocks of 128 threads) or the whole block owns a row; each of its threads holds VPT vectors of V elements.
@@ -215,6 +322,7 @@ row_kernel(const RowArgs a) {
   __shared__ float s_sum[kMaxWarps];
   __shared__ uint32_t s_max[kMaxWarps];
   __shared__ unsigned long long s_top;
+  __shared__ float s_wide[kMaxWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int gt = WARP_ROW ? lane : threadIdx.x;
   const int gsize = WARP_ROW ? 32 : blockDim.x;
@@ -354,7 +462,22 @@ row_kernel(const RowArgs a) {
     }
     if (kCodes) top = __reduce_max_sync(0xffffffffu, lane < nw ? s_max[lane] : 0u);
   }
-  const float rms = kScaled ? rsqrtf(ss * a.inv_width + a.eps) : 1.f;
+  const float mean = ss * a.inv_width + a.eps;
+  float rms = kScaled ? rsqrtf(mean) : 1.f;
+  // the mean is no number of [kLeastMean, infinity), as one comparison of its bits; the same for the whole row
+  const bool wide = kScaled && __float_as_uint(mean) - __float_as_uint(kLeastMean) >= 0x7f800000u - __float_as_uint(kLeastMean);
+  auto shifted_squares = [&](float shift) {
+    const uint64_t shift2 = f2_pack(shift, shift);
+    uint64_t s2 = 0;
+#pragma unroll
+    for (int p = 0; p < (kScaled ? E / 2 : 0); ++p) {
+      const uint64_t u = f2_mul(v[p], shift2);
+      s2 = f2_fma(u, u, s2);
+    }
+    float lo, hi;
+    f2_unpack(s2, lo, hi);
+    return lo + hi;
+  };
 
   T* sum = kScaled && a.sum_out ? static_cast<T*>(a.sum_out) + row * a.sum_stride : nullptr;
   auto store_chunk = [&](T* p, int k, const uint64_t* t) {
@@ -376,7 +499,21 @@ row_kernel(const RowArgs a) {
 
   if (MODE == kNorm) {
     T* out = static_cast<T*>(a.out) + row * a.out_stride;
+    // rows that take many registers leave them to a call (fp32 37000 x 5120: 220 us, 235 in place), others do it in place (bf16
+    // 37000 x 1002 with the residual: 52 us, 57 with the call)
+    if constexpr (E >= 16) {
+      if (wide) {
+        wide_norm<T, V, WARP_ROW>(x, r, w, sum, out, gt * V, a.width, gsize * V, a.inv_width, a.eps, mean, s_wide);
+        return;
+      }
+    }
     store_sum();
+    if (E < 16 && wide) {
+      const float shift = wide_shift(mean);
+      rms = wide_root<WARP_ROW>(shifted_squares(shift), shift, a.inv_width, a.eps, s_wide);
+#pragma unroll
+      for (int p = 0; p < E / 2; ++p) v[p] = f2_mul(v[p], f2_pack(shift, shift));
+    }
     const uint64_t rms2 = f2_pack(rms, rms);
     for_chunks([&](int k, uint64_t (&t)[kChunk / 2]) {
 #pragma unroll
@@ -397,9 +534,14 @@ row_kernel(const RowArgs a) {
     store_sum();
     return;
   }
-  if (gt == 0) a.scale[row] = m * (1.f / 127.f) * (m > 0.f ? rms : 1.f);
   // below 1e-30 fp32 may lose more than kNear (subnormal t, 127 / m infinite): every code in fp64, by division
   const bool tiny = m > 0.f && m < 1e-30f;
+  if (kScaled && (wide || tiny)) {
+    wide_codes<T, V, WARP_ROW>(x, r, w, sum, q, a.scale + row, gt * V, a.width, gsize * V, a.inv_width, a.eps, wide ? wide_shift(mean) : 1.f,
+                               s_wide, &s_top);
+    return;
+  }
+  if (gt == 0) a.scale[row] = m * (1.f / 127.f) * (m > 0.f ? rms : 1.f);
   const float inv = m >= 1e-30f ? 127.f / m : 0.f;
   uint32_t open = 0;   // vectors of this thread with an element next to a border, or all of them
   const uint64_t inv2 = f2_pack(inv, inv), round2 = f2_pack(kRound, kRound), minus2 = f2_pack(-1.f, -1.f);
@@ -432,14 +574,14 @@ row_kernel(const RowArgs a) {
       if (c < a.width) P::store_codes(q + c, code + e);
     }
   });
-  if (tiny) open = ~0u >> (32 - VPT);
+  if (!kScaled && tiny) open = ~0u >> (32 - VPT);
 
   const bool any = !kScaled ? open != 0 : WARP_ROW ? __any_sync(0xffffffffu, open != 0) : __syncthreads_or(open != 0);
   if (any) {
     double m64 = m;
     if (MODE == kNormI8) {
       unsigned long long best = 0;
-      const float close = tiny ? 0.f : m * (1.f - 4.76837158e-7f);   // 1 - 2^-21
+      const float close = m * (1.f - 4.76837158e-7f);   // 1 - 2^-21
       if (__uint_as_float(mine) >= close) {
         uint32_t near = 0;   // vectors with an element this close to the maximum
         for_chunks([&](int k, uint64_t (&t)[kChunk / 2]) {
@@ -457,7 +599,7 @@ row_kernel(const RowArgs a) {
           const int c = column(__ffs((int)near) - 1);
           if (c >= a.width) continue;
           double t[V];
-          exact_t<T, V>(a, x, r, w, c, t);
+          exact_t<T, V>(x, r, w, c, t);
 #pragma unroll
           for (int e = 0; e < V; ++e) best = max(best, (unsigned long long)__double_as_longlong(fabs(t[e])));
         }
@@ -477,11 +619,11 @@ row_kernel(const RowArgs a) {
       const int c = column(__ffs((int)open) - 1);
       if (c >= a.width) continue;
       uint32_t code[V];
-      if (tiny) {
-        double t[V];
-        exact_t<T, V>(a, x, r, w, c, t);
+      if (!kScaled && tiny) {
+        float f[V];
+        P::unpack(P::load(x + x_offset(a, c)), f);
 #pragma unroll
-        for (int e = 0; e < V; ++e) code[e] = (uint32_t)(int)rint(127.0 * t[e] / m64);
+        for (int e = 0; e < V; ++e) code[e] = (uint32_t)(int)rint(127.0 * (double)f[e] / m64);
       } else if (MODE == kQuantI8) {
         // t and m are exact, so fp32 tells the side: 254 |t| against (2k + 1) m, the product in two parts, both
         // scaled down so that neither overflows
@@ -496,7 +638,7 @@ row_kernel(const RowArgs a) {
         }
       } else {
         double t[V];
-        exact_t<T, V>(a, x, r, w, c, t);
+        exact_t<T, V>(x, r, w, c, t);
 #pragma unroll
         for (int e = 0; e < V; ++e) {   // k or k + 1, by the side of the border between them; on it, the even one
           const double size = 127.0 * fabs(t[e]);

@@ -1,0 +1,93 @@
+"""Norms of finite rows anywhere in fp32's range, against the fp64 oracle: rows whose squares or whose sum of squares
+fp32 cannot hold, beside ordinary ones in the same call.
+
+Tolerances are those of test_gpu_layer.py's docstring (the statistics of such rows are held in more bits, not fewer), and where
+numbers are subnormal, half a step there: 2^-150 for fp32, 2^-134 for bf16.  A norm's product v w may be one while the output is
+not: its half step is then multiplied by the root, which is at most 2^50 where the product is formed in fp32.
+"""
+import numpy as np
+import pytest
+import torch
+
+import block_sparse_cluster_b200 as da
+import oracle
+from tests.test_gpu_layer import BF16, F32, _close, _cuda, _gen, _half
+
+pytestmark = pytest.mark.gpu
+
+# powers of two of the rows: squares below fp32's smallest number, subnormal ones, the sums' borders, sums above the largest
+EXPONENTS = [0, -146, -130, -110, -75, -66, -60, -52, -50, -49, -48, 3, 55, 57, 59, 62, 63, 64, 70, 100, 122, 0]
+
+
+def _rows(width, dtype, seed):
+    g = _gen(seed)
+    power = torch.tensor([2.0 ** e for e in EXPONENTS], dtype=torch.float64)[:, None]
+    x = torch.randn(len(EXPONENTS), width, generator=g, dtype=torch.float64).clamp(-8, 8) * power
+    r = torch.randn(len(EXPONENTS), width, generator=g, dtype=torch.float64).clamp(-8, 8) * power
+    w = 1 + 0.2 * torch.randn(width, generator=g, dtype=torch.float64)
+    return x.to(dtype), r.to(dtype), w.to(dtype)
+
+
+@pytest.mark.parametrize("eps", [0.0, 1e-6, 1e20, 3e38])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("width", [1, 64, 77, 512, 1536, 2056, 4100, 5120, 9002, 16383, 16384])
+def test_norm_of_rows_of_any_size(width, dtype, eps):
+    x, r, w = _rows(width, dtype, width)
+    rows = x.shape[0]
+    for residual, weight in ((None, None), (r, w)):
+        xc, rc, wc = x.cuda(), _cuda(residual), _cuda(weight)
+        out, total = torch.empty_like(xc), None if residual is None else torch.empty_like(xc)
+        da.da_rms_norm(xc, wc, out, residual=rc, sum_out=total, eps=eps)
+        with np.errstate(divide="ignore", invalid="ignore"):
+            ref, v = oracle.rms_norm(x, residual, weight, eps)
+            root = np.minimum(1 / np.sqrt((v * v).mean(-1, keepdims=True) + eps), 2.0 ** 50)
+        some = np.isfinite(ref).all(-1) & (np.abs(v).max(-1) > 0)       # eps = 0 and a row of nothing but zeros: 0 / 0
+        assert some.sum() >= rows - 2
+        tol = np.abs(ref) * (2.0 ** -19 + _half(dtype) * 1.001) + _half_step_of_least(dtype) + 2.0 ** -150 * root
+        _close(out[torch.from_numpy(some)], ref[some], tol[some])
+        q, scale = torch.empty(rows, width, dtype=torch.int8, device="cuda"), torch.empty(rows, device="cuda")
+        total2 = None if residual is None else rc                       # the residual stream in place
+        da.da_rms_norm_i8(xc, wc, q, scale, residual=rc, sum_out=total2, eps=eps)
+        with np.errstate(divide="ignore", invalid="ignore"):
+            rq, rs, _ = oracle.rms_norm_i8(x, residual, weight, eps)
+        rs = np.where(np.abs(v).max(-1) > 0, rs, 0.0)                   # a row of zeros has scale 0
+        assert np.array_equal(q.cpu().numpy().astype(np.int64), rq)
+        _close(scale, rs, rs * 2.0 ** -19 + 2.0 ** -149)
+        if residual is not None:
+            assert torch.equal(total2, total)
+            _close(total, v, np.abs(v) * _half(dtype) * 1.001 + 2.0 ** -24 * np.abs(v) + _half_step_of_least(dtype))
+
+
+def _half_step_of_least(dtype):
+    """Half a step of the type's subnormal numbers, and of fp32's for the value that is rounded to it."""
+    return 2.0 ** -134 + 2.0 ** -150 if dtype == BF16 else 2.0 ** -149
+
+
+@pytest.mark.parametrize("width", [64, 16384])
+def test_sums_beyond_fp32_at_any_width(width):
+    """One element that overflows by its own square, and many that do so together."""
+    x = torch.full((3, width), 1.5e17)
+    x[1] = 0
+    x[1, 5] = 3e20
+    x[2] = 1.0
+    q, scale, out = torch.empty(3, width, dtype=torch.int8, device="cuda"), torch.empty(3, device="cuda"), torch.empty(3, width, device="cuda")
+    da.da_rms_norm_i8(x.cuda(), None, q, scale)
+    da.da_rms_norm(x.cuda(), None, out)
+    rq, rs, _ = oracle.rms_norm_i8(x)
+    assert np.array_equal(q.cpu().numpy().astype(np.int64), rq)
+    _close(scale, rs, rs * 2.0 ** -19)
+    ref = oracle.rms_norm(x)[0]
+    _close(out, ref, np.abs(ref) * 2.0 ** -18)
+
+
+@pytest.mark.parametrize("width", [64, 77, 4096])
+def test_products_below_fp32(width):
+    """A weight so small that v * w is no fp32 number, though the output is."""
+    g = _gen(width)
+    x = torch.randn(4, width, generator=g) * torch.tensor([1e-30, 1e-25, 1e-20, 1e-38])[:, None]
+    w = (1 + torch.rand(width, generator=g)) * 1e-25
+    q, scale = torch.empty(4, width, dtype=torch.int8, device="cuda"), torch.empty(4, device="cuda")
+    da.da_rms_norm_i8(x.cuda(), w.cuda(), q, scale, eps=0.0)
+    rq, rs, _ = oracle.rms_norm_i8(x, None, w, 0.0)
+    assert np.array_equal(q.cpu().numpy().astype(np.int64), rq)
+    _close(scale, rs, rs * 2.0 ** -19)

@@ -23,10 +23,10 @@
 // 338 us against 264 then; norm: 481 against 451): the registers of the loads ahead cost more warps than they hide.
 //
 // Measured, bf16: norm with residual 75600 x 5120 451 us (6.86 TB/s, 1.07 of the plain copy's rate); codes of the norm with
-// residual 75600 x 1536 129 us (6.3 TB/s), x 5120 503 us (5.4 TB/s: two barriers a row, and a third for the 46 % of the
+// residual 75600 x 1536 130-135 us (6.0 TB/s), x 5120 420-455 us (6.2 TB/s: two barriers a row, and a third for the 46 % of the
 // rows that need a second look); codes of 40 heads of 75600 tokens 194 us (6.0 TB/s).  Rows that do not start on 16 bytes are
-// walked in pairs (bf16, even) or element by element: norm with residual 75600 x 1001 185 us in bf16 (0.5 of the copy's
-// rate) and 187 in fp32 (1.0), codes 290 and 261 (0.3 and 0.6).
+// walked in pairs (bf16, even) or element by element: norm with residual 75600 x 1001 187 us in bf16 (0.5 of the copy's
+// rate) and 189 in fp32 (1.0), codes 263 and 258 (0.3 and 0.6).
 #include "da_common.cuh"
 #include "da_internal.h"
 
@@ -257,10 +257,10 @@ __device__ __noinline__ void wide_norm(const T* x, const T* r, const T* w, T* su
 }
 
 // The norm's codes, scale and sum of a row of which fp32 loses the statistics or the t; as in wide_norm.  top: zero, the
-// block's scratch, when it owns the row.
+// block's scratch, when it owns the row.  In place: a call costs the rows around it more (75600 x 2048: 211 us, 183 so).
 template <typename T, int V, bool WARP_ROW>
 __device__ __forceinline__ void wide_codes(const T* x, const T* r, const T* w, T* sum, int8_t* q, float* scale, int first, int width, int step,
-                                        float inv_width, float eps, float shift, float* part, unsigned long long* top) {
+                                           float inv_width, float eps, float shift, float* part, unsigned long long* top) {
   using P = Pack<T, V>;
   float squares = 0.f;
   unsigned long long best = 0;   // bits of max |t|, which order as integers

@@ -322,9 +322,9 @@ typedef struct {
  * dtype, rows their stride apart; weight: [width] of dtype (NULL: ones).  v, the sum of squares and
  * the products are held in fp32 (v is not rounded to dtype before the norm); out and sum_out are rounded
  * once.  out may be x or residual, sum_out may be x or residual (the residual stream updated in
- * place), but not the same buffer.  width <= 16384 (DA_ERR_UNSUPPORTED above); eps >= 0.  A row with an infinity
- * or NaN gives what the formula gives in fp32; so does one whose sum of squares leaves fp32's range (|v| above about 1e18, or,
- * with eps = 0, below about 1e-22).
+ * place), but not the same buffer.  width <= 16384 (DA_ERR_UNSUPPORTED above); eps >= 0.  Finite rows may be of
+ * any size: where squares or their sum are no fp32 numbers, they are taken of v times a power of two.  A row with an
+ * infinity or NaN (x + residual beyond fp32 is one) gives what the formula gives in fp32.
  */
 DA_API da_status da_rms_norm(int64_t rows, int width, da_dtype dtype, const void* x, int64_t x_stride,
                              const void* residual, int64_t residual_stride, const void* weight, float eps,
@@ -336,7 +336,7 @@ DA_API da_status da_rms_norm(int64_t rows, int width, da_dtype dtype, const void
  *   q = nearest integer to 127 t / m (ties to even),   scale = m / (127 sqrt(mean(v^2) + eps)),
  * so that q * scale is the norm's output to half a step.  q is taken from the exact quotient (fp64
  * where fp32 cannot tell the two sides of a border apart).  A row of zeros gives q = 0, scale = 0; a row with an
- * infinity or NaN (or whose t leaves fp32's range) gives q = 0, scale = NaN, so that products of it
+ * infinity or NaN (or whose v or t exceeds fp32's largest number) gives q = 0, scale = NaN, so that products of it
  * are NaN.  q: [rows, width] int8, q_stride elements apart (a multiple of 16 suits da_linear_i8); bytes
  * between width and q_stride are left as they were.  scale: [rows] fp32.  Other arguments and errors as in da_rms_norm,
  * but q and scale share memory with nothing.

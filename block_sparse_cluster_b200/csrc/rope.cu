@@ -9,6 +9,9 @@
 // frequency modulo 2^64 is what is left of the angle after its whole turns, exactly, however far the position and whatever
 // its sign.  Only the upper 32 bits, as half turns in [-1, 1), are rounded to fp32 for sincospif.
 //
+// A norm whose mean square (with eps) leaves [kLeastMean, fp32's largest number) is taken again of x times a power of two, as
+// the row operators' norms are.
+//
 // The kernel is bound by HBM: x is read once and out written once.  A thread's unit of work is two
 // 16-byte vectors of a head, elements [j, j + V) and [j + d/2, j + d/2 + V): whole pairs in either pairing.
 // A group of threads owns a token, all its heads (the norm over all heads needs them together); every unit of a
@@ -16,7 +19,7 @@
 // of tokens: the block forms the angles of all of them first, and each thread keeps the loads of the next kStages tokens
 // in flight with cp.async, into shared memory that only it reads: loads ahead cost no registers and need no barrier.
 //
-// Measured, bf16, 40 heads of 128 and 75600 tokens (floor 241 us): 239 us without a norm, 245 with the head's, 247 with the
+// Measured, bf16, 40 heads of 128 and 75600 tokens (floor 241 us): 240 us without a norm, 246 with the head's, 255 with the
 // norm over all heads, whose barrier a token is what is left; 12 heads, 32760 tokens (floor 31 us): 35, 37 and 42 us, where
 // a token is 96 threads' work of 16 elements and its fixed instructions show.  fp32 runs at the copy's rate.
 #include <math.h>
@@ -146,6 +149,16 @@ struct Unit<float, HALVES> {
   }
 };
 
+// 2^-100: squares below fp32's normal numbers, each off by up to 2^-150, are not seen in such a mean.
+constexpr float kLeastMean = 0x1p-100f;
+__device__ __forceinline__ bool leaves_fp32(float mean) {   // as one comparison of the bits; a NaN does too
+  return __float_as_uint(mean) - __float_as_uint(kLeastMean) >= 0x7f800000u - __float_as_uint(kLeastMean);
+}
+// The power of two that brings x into range.  Above: some |x| >= 2^57 (2^14 elements), and 2^14 (2^(128 - 72))^2 is still
+// a number; elements that fall below 2^-126 by it are 2^110 below the rest.  Below: |x| < 2^-43, whose squares then sum to less
+// than 2^114, and nothing is lost.
+__device__ __forceinline__ float wide_shift(float mean) { return !leaves_fp32(mean) ? 1.f : mean < kLeastMean ? 0x1p100f : 0x1p-72f; }
+
 // UPT: units a thread holds of a token.
 template <typename T, int D, int UPT, bool HALVES, bool NORMED>
 __global__ void __launch_bounds__(512) rope_kernel(const __grid_constant__ RopeArgs a) {
@@ -159,6 +172,7 @@ __global__ void __launch_bounds__(512) rope_kernel(const __grid_constant__ RopeA
   __shared__ uint64_t s_freq[D / 2];
   __shared__ unsigned char s_axis[D / 2];
   __shared__ __align__(16) float s_part[2][16];
+  __shared__ float s_wide[16];
   const int b = blockIdx.y, n0 = blockIdx.x * a.run, h0 = blockIdx.z * a.heads_per_block;
   const int run = min(a.run, a.N - n0);
   const int units = min(a.heads_per_block, a.H - h0) * kPerHead;
@@ -231,6 +245,26 @@ __global__ void __launch_bounds__(512) rope_kernel(const __grid_constant__ RopeA
   }
   __syncthreads();
 
+  auto squares = [](const uint4 (&unit)[2]) {
+    uint64_t va[V / 2], vb[V / 2], s2 = 0;
+    U::unpack(unit, va, vb);
+#pragma unroll
+    for (int e = 0; e < V / 2; ++e) s2 = f2_fma(va[e], va[e], f2_fma(vb[e], vb[e], s2));
+    float lo, hi;
+    f2_unpack(s2, lo, hi);
+    return lo + hi;
+  };
+  auto times = [](uint4 (&unit)[2], float shift) {
+    uint64_t va[V / 2], vb[V / 2];
+    U::unpack(unit, va, vb);
+#pragma unroll
+    for (int e = 0; e < V / 2; ++e) {
+      va[e] = f2_mul(va[e], f2_pack(shift, shift));
+      vb[e] = f2_mul(vb[e], f2_pack(shift, shift));
+    }
+    U::pack(va, vb, unit);
+  };
+
   // every group takes the same number of turns, so that the barriers match
   uint4 raw[UPT][2];
 #pragma unroll
@@ -250,13 +284,7 @@ __global__ void __launch_bounds__(512) rope_kernel(const __grid_constant__ RopeA
       }
       factor[i] = 1.f;
       if (NORMED) {
-        uint64_t va[V / 2], vb[V / 2], s2 = 0;
-        U::unpack(raw[i], va, vb);
-#pragma unroll
-        for (int e = 0; e < V / 2; ++e) s2 = f2_fma(va[e], va[e], f2_fma(vb[e], vb[e], s2));
-        float lo, hi;
-        f2_unpack(s2, lo, hi);
-        factor[i] = lo + hi;
+        factor[i] = squares(raw[i]);
         ss += factor[i];
       }
     }
@@ -265,7 +293,16 @@ __global__ void __launch_bounds__(512) rope_kernel(const __grid_constant__ RopeA
       for (int i = 0; i < UPT; ++i) {
 #pragma unroll
         for (int o = kPerHead / 2; o > 0; o >>= 1) factor[i] += __shfl_xor_sync(0xffffffffu, factor[i], o);
-        factor[i] = rsqrtf(factor[i] * (1.f / D) + a.eps);
+        float mean = factor[i] * (1.f / D) + a.eps;
+        if (__any_sync(0xffffffffu, has(i) && leaves_fp32(mean))) {
+          const float shift = wide_shift(mean);
+          times(raw[i], shift);
+          float s2 = squares(raw[i]);
+#pragma unroll
+          for (int o = kPerHead / 2; o > 0; o >>= 1) s2 += __shfl_xor_sync(0xffffffffu, s2, o);
+          mean = s2 * (1.f / D) + a.eps * shift * shift;
+        }
+        factor[i] = rsqrtf(mean);
       }
     } else if (NORMED) {
       for (int o = min(a.group, 32) / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
@@ -278,7 +315,25 @@ __global__ void __launch_bounds__(512) rope_kernel(const __grid_constant__ RopeA
           ss += (p.x + p.y) + (p.z + p.w);
         }
       }
-      const float f = rsqrtf(ss * a.inv_width + a.eps);
+      float mean = ss * a.inv_width + a.eps;
+      if (__any_sync(0xffffffffu, leaves_fp32(mean))) {   // in all warps of a block that is the group
+        const float shift = wide_shift(mean);
+        ss = 0.f;
+#pragma unroll
+        for (int i = 0; i < UPT; ++i) {
+          times(raw[i], shift);
+          ss += squares(raw[i]);
+        }
+        for (int o = min(a.group, 32) / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+        if (a.group > 32) {   // the next sum comes here only behind the next token's barrier
+          if ((threadIdx.x & 31) == 0) s_wide[threadIdx.x >> 5] = ss;
+          __syncthreads();
+          ss = 0.f;
+          for (int w = 0; w < blockDim.x >> 5; ++w) ss += s_wide[w];
+        }
+        mean = ss * a.inv_width + a.eps * shift * shift;
+      }
+      const float f = rsqrtf(mean);
 #pragma unroll
       for (int i = 0; i < UPT; ++i) factor[i] = f;
     }

@@ -402,7 +402,8 @@ typedef struct {
  * the grid (text behind a video) are not turned: they are copied, or normed only.
  * weight: NULL, or the norm's weight of dtype, with x first replaced by x / sqrt(mean(x^2) + eps) *
  * weight: the mean over the head's d elements if weight_width = d, over all of a token's heads if
- * weight_width = H * d (<= 16384).  Angles lose no whole turn at any position; norm and rotation are in fp32, rounded once.
+ * weight_width = H * d (<= 16384).  Angles lose no whole turn at any position; norm (of finite values of any size) and
+ * rotation are in fp32, rounded once.
  * out may be x.
  */
 DA_API da_status da_rope(const da_rope_plan* plan, int B, int H, int N, int d, da_dtype dtype, const void* x,

@@ -11,7 +11,7 @@ import torch
 
 import block_sparse_cluster_b200 as da
 import oracle
-from tests.test_gpu_layer import BF16, F32, _close, _cuda, _gen, _half
+from tests.test_gpu_layer import BF16, F32, _close, _cuda, _gen, _half, _rope_check
 
 pytestmark = pytest.mark.gpu
 
@@ -91,3 +91,29 @@ def test_products_below_fp32(width):
     rq, rs, _ = oracle.rms_norm_i8(x, None, w, 0.0)
     assert np.array_equal(q.cpu().numpy().astype(np.int64), rq)
     _close(scale, rs, rs * 2.0 ** -19)
+
+
+@pytest.mark.parametrize("eps", [0.0, 1e-6, 1e20])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("norm", ["head", "full"])
+@pytest.mark.parametrize("B,H,N,d,axes", [(1, 1, 44, 64, (32, 16, 16)), (2, 3, 23, 64, (22, 20, 22)), (1, 12, 22, 128, (44, 42, 42)), (1, 40, 22, 128, (16, 56, 56)),
+                                          (1, 128, 22, 128, (42, 44, 42))])
+def test_rope_after_a_norm_of_any_size(B, H, N, d, axes, norm, dtype, eps):
+    """Heads (or whole tokens, where the norm is over all heads) of every size side by side."""
+    g = _gen(H)
+    power = torch.tensor([2.0 ** e for e in EXPONENTS], dtype=torch.float64)
+    n, h = torch.arange(N)[:, None], torch.arange(H)[None]
+    which = (n + (0 if norm == "full" else 5) * h) % len(EXPONENTS)
+    x = torch.randn(B, H, N, d, generator=g, dtype=torch.float64).clamp(-8, 8) * power[which.expand(N, H)].T[None, :, :, None]
+    x = x.to(dtype).cuda()
+    weight = (1 + 0.2 * torch.randn(d if norm == "head" else H * d, generator=g)).to(dtype).cuda()
+    for pairing in ("adjacent", "halves"):
+        rope = da.Rope(axes=axes, grid=(2, 2, 5), pairing=pairing)      # the tokens behind the grid are normed only
+        out = torch.empty_like(x)
+        da.da_rope(x, out, rope, weight=weight, eps=eps)
+        zero = (x == 0).all(-1) if norm == "head" else (x == 0).all(-1).all(1, keepdim=True).expand(B, H, N)
+        if eps == 0:                                                    # 0 / 0
+            assert torch.isnan(out[zero]).all()
+            out[zero] = 0
+        with np.errstate(divide="ignore", invalid="ignore"):
+            _rope_check(x, out, rope, None, weight, max(eps, 1e-300), dtype)

@@ -8,6 +8,7 @@ import concurrent.futures as cf
 import glob
 import importlib.util
 import os
+import shutil
 import subprocess
 import sys
 import sysconfig
@@ -49,14 +50,22 @@ def _link(objs, lib):
         raise RuntimeError(f"nvcc link of {os.path.basename(lib)} failed")
 
 
+def _cuda_include():
+    """CUDA's headers: beside nvcc, which may be a name on PATH or a link, or else those of CUDA_HOME or the usual place."""
+    nvcc = shutil.which(NVCC) or NVCC
+    homes = [os.path.dirname(os.path.dirname(p)) for p in (os.path.realpath(nvcc), os.path.abspath(nvcc))]
+    homes += [os.environ.get("CUDA_HOME", ""), "/usr/local/cuda"]
+    dirs = [os.path.join(h, "include") for h in homes if h]
+    return next((d for d in dirs if os.path.exists(os.path.join(d, "cuda_runtime.h"))), dirs[0])
+
+
 def build_call():
     """Compile the layer operators' marshalling module (host code against torch's and Python's headers)."""
     torch = os.path.dirname(importlib.util.find_spec("torch").origin)
-    cuda = os.path.dirname(os.path.dirname(NVCC))
     cmd = ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden",
            *["-I" + d for d in (os.path.join(ROOT, "include"), os.path.join(torch, "include"),
                                 os.path.join(torch, "include", "torch", "csrc", "api", "include"),
-                                sysconfig.get_paths()["include"], os.path.join(cuda, "include"))],
+                                sysconfig.get_paths()["include"], _cuda_include())],
            CALL_SRC, "-o", CALL_LIB, "-L" + os.path.join(torch, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:

@@ -21,6 +21,7 @@ LIB = os.path.join(HERE, "libda.so")
 FAULT_LIB = os.path.join(HERE, "libda_fault.so")
 CALL_SRC = os.path.join(CSRC, "layer_call.cpp")
 CALL_LIB = os.path.join(HERE, "_layer_call.so")
+CALL_STAMP = "layer_call.built_for"   # in BUILD
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-fvisibility=hidden",
@@ -73,10 +74,22 @@ def build_call():
         raise RuntimeError("g++ failed: layer_call.cpp")
 
 
+def _built_for():
+    """What the marshalling module is tied to beside its sources: this torch and this Python."""
+    version = os.path.join(os.path.dirname(importlib.util.find_spec("torch").origin), "version.py")
+    return f"{sysconfig.get_config_var('SOABI')}\n{open(version).read() if os.path.exists(version) else ''}"
+
+
+def _call_is_current(deps):
+    stamp = os.path.join(BUILD, CALL_STAMP)
+    return (os.path.exists(CALL_LIB) and os.path.getmtime(CALL_LIB) >= deps and os.path.exists(stamp)
+            and open(stamp).read() == _built_for())
+
+
 def build(verbose=False, force=False, extra=()):
     """Compile every csrc/*.cu for sm_100a and link libda.so, the layer operators' marshalling module
     _layer_call.so, and the test build libda_fault.so (the same sources with DA_FAULT_INJECT defined: one withheld barrier arrival, for the test of
-    the bounded device waits); skip what is up to date."""
+    the bounded device waits); skip what is up to date (the module is not for another torch or Python than it was built for)."""
     os.makedirs(BUILD, exist_ok=True)
     deps = _deps_mtime()
     if force or not os.path.exists(LIB) or os.path.getmtime(LIB) < deps:
@@ -90,8 +103,10 @@ def build(verbose=False, force=False, extra=()):
         if failed:
             raise RuntimeError("nvcc failed: " + ", ".join(os.path.basename(f[0]) for f in failed))
         _link([r[1] for r in results], LIB)
-    if force or not os.path.exists(CALL_LIB) or os.path.getmtime(CALL_LIB) < deps:
+    if force or not _call_is_current(deps):
         build_call()
+        with open(os.path.join(BUILD, CALL_STAMP), "w") as f:
+            f.write(_built_for())
     if force or not os.path.exists(FAULT_LIB) or os.path.getmtime(FAULT_LIB) < deps:
         # only the attention kernel differs in the test build
         src = os.path.join(CSRC, "attention_tc.cu")

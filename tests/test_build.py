@@ -55,3 +55,31 @@ def test_headers_are_found_however_nvcc_is_named(how, tmp_path, monkeypatch):
         monkeypatch.setenv("CUDA_HOME", str(tmp_path / "toolkit"))
     found = _includes(_build_module(monkeypatch, name), monkeypatch)
     assert str(tmp_path / "toolkit" / "include") in [os.path.realpath(d) for d in found]
+
+
+def test_marshalling_module_is_built_again_for_another_torch(tmp_path, monkeypatch):
+    """Sources untouched: built for the first time, kept, and built again once torch or Python is another."""
+    module = _build_module(monkeypatch, "nvcc")
+    for name in ("LIB", "FAULT_LIB", "CALL_LIB"):
+        path = tmp_path / name
+        path.write_text("")
+        monkeypatch.setattr(module, name, str(path))
+    monkeypatch.setattr(module, "BUILD", str(tmp_path / "_build"))
+    torch = tmp_path / "torch"
+    torch.mkdir()
+    (torch / "__init__.py").write_text("")
+    (torch / "version.py").write_text("__version__ = '1'\n")
+    monkeypatch.setattr(module.importlib.util, "find_spec", lambda name: importlib.util.spec_from_file_location(name, torch / "__init__.py"))
+    built = []
+    monkeypatch.setattr(module, "build_call", lambda: built.append(1))
+    module.build()
+    assert built == [1]                      # a module that is not known to be this torch's
+    module.build()
+    assert built == [1]
+    (torch / "version.py").write_text("__version__ = '2'\n")
+    module.build()
+    module.build()
+    assert built == [1, 1]
+    monkeypatch.setattr(module.sysconfig, "get_config_var", lambda name: "another")
+    module.build()
+    assert built == [1, 1, 1]

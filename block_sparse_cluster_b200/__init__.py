@@ -330,12 +330,25 @@ def da_noalloc_device_status(stream=None) -> int:
 # shapes, strides and devices, in a compiled module (csrc/layer_call.cpp), since the smallest of these calls are bound by
 # the host.  They run on the tensors' device, on its current stream by default.
 
+class _Unloaded:
+    """In the module's place when it does not load (built for another torch, say): the attention needs none of it."""
+
+    def __init__(self, why):
+        self._why = why
+
+    def __getattr__(self, name):
+        raise ImportError(f"_layer_call.so does not load ({self._why}); run python block_sparse_cluster_b200/build.py") from self._why
+
+
 try:
     from . import _layer_call
 except ImportError as e:
-    raise ImportError("_layer_call.so is not built or does not load; run python block_sparse_cluster_b200/build.py") from e
-_layer_call.bind(DAError, {name: ctypes.cast(getattr(_lib, name), _P).value for name in
-                           ("da_rms_norm", "da_rms_norm_i8", "da_quantize_i8", "da_linear_i8", "da_rope")})
+    if not os.path.exists(os.path.join(os.path.dirname(os.path.abspath(__file__)), "_layer_call.so")):
+        raise ImportError("_layer_call.so is not built; run python block_sparse_cluster_b200/build.py") from e
+    _layer_call = _Unloaded(e)
+else:
+    _layer_call.bind(DAError, {name: ctypes.cast(getattr(_lib, name), _P).value for name in
+                               ("da_rms_norm", "da_rms_norm_i8", "da_quantize_i8", "da_linear_i8", "da_rope")})
 
 
 def da_rms_norm(x: torch.Tensor, weight: Optional[torch.Tensor], out: torch.Tensor,

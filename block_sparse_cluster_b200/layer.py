@@ -56,6 +56,7 @@ class DecoupledLayer:
 
     The attention engine is ``engine`` (its plan is prepared once with ``prepare``); Q, K and V of
     the last ``project`` are ``Q``, ``K`` and ``V`` [B,H,N,d], for the initial clustering of the keys.
+    Every call makes the layer's device current, whose current stream is the default one.
     """
 
     def __init__(self, dims: Dims, width: int, weights: LayerWeights, rope: Rope, eps: float = 1e-6, device="cuda"):
@@ -73,8 +74,13 @@ class DecoupledLayer:
         self._qk = torch.empty(tokens, 2 * channels, **like)
         self.Q, self.K, self.V, self.O = (torch.empty(B, H, N, d, **like) for _ in range(4))
 
+    def _on_device(self):
+        # the attention's calls run on the current device, unlike the layer operators, which run on their tensors'
+        return torch.cuda.device(self.Q.device)
+
     def prepare(self, kv_idx: torch.Tensor, kv_cnt: torch.Tensor, stream=None):
-        return self.engine.prepare(kv_idx, kv_cnt, stream)
+        with self._on_device():
+            return self.engine.prepare(kv_idx, kv_cnt, stream)
 
     def project(self, x: torch.Tensor, residual: Optional[torch.Tensor] = None, stream=None) -> None:
         """Hidden states x [B, N, width] to Q, K and V.  With a residual stream [B, N, width], which
@@ -82,21 +88,23 @@ class DecoupledLayer:
         w, (B, H, N, d) = self.weights, self.Q.shape
         rows = x.view(B * N, self.width)
         total = None if residual is None else residual.view(B * N, self.width)
-        da_rms_norm_i8(rows, w.norm, self._x, self._x_scale, residual=total, sum_out=total, eps=self.eps, stream=stream)
-        ws = self.engine.ws
-        da_linear_i8(self._x, self._x_scale, *w.qk, self._qk, ws, bias=w.qk_bias, stream=stream)
-        da_linear_i8(self._x, self._x_scale, *w.v, self.V, ws, bias=w.v_bias, stream=stream)
-        slots = self._qk.view(B, N, 2, H, d)
-        for slot, norm, out in ((0, w.q_norm, self.Q), (1, w.k_norm, self.K)):
-            da_rope(slots[:, :, slot].permute(0, 2, 1, 3), out, self.rope, weight=norm, eps=self.eps, stream=stream)
+        with self._on_device():
+            da_rms_norm_i8(rows, w.norm, self._x, self._x_scale, residual=total, sum_out=total, eps=self.eps, stream=stream)
+            ws = self.engine.ws
+            da_linear_i8(self._x, self._x_scale, *w.qk, self._qk, ws, bias=w.qk_bias, stream=stream)
+            da_linear_i8(self._x, self._x_scale, *w.v, self.V, ws, bias=w.v_bias, stream=stream)
+            slots = self._qk.view(B, N, 2, H, d)
+            for slot, norm, out in ((0, w.q_norm, self.Q), (1, w.k_norm, self.K)):
+                da_rope(slots[:, :, slot].permute(0, 2, 1, 3), out, self.rope, weight=norm, eps=self.eps, stream=stream)
 
     def attend(self, centroids: torch.Tensor, out: torch.Tensor, stream=None) -> torch.Tensor:
         """Attention of the projected Q, K and V, and its projection into out [B, N, width]."""
         w, (B, H, N, d) = self.weights, self.Q.shape
-        self.engine.step(self.Q, self.K, self.V, centroids, self.O, stream=stream)
-        da_quantize_i8(self.O, self._o, self._o_scale, stream=stream)
-        da_linear_i8(self._o, self._o_scale, *w.out, out.view(B * N, self.width), self.engine.ws, bias=w.out_bias,
-                     stream=stream)
+        with self._on_device():
+            self.engine.step(self.Q, self.K, self.V, centroids, self.O, stream=stream)
+            da_quantize_i8(self.O, self._o, self._o_scale, stream=stream)
+            da_linear_i8(self._o, self._o_scale, *w.out, out.view(B * N, self.width), self.engine.ws, bias=w.out_bias,
+                         stream=stream)
         return out
 
     def step(self, x: torch.Tensor, centroids: torch.Tensor, out: torch.Tensor,
@@ -105,4 +113,5 @@ class DecoupledLayer:
         return self.attend(centroids, out, stream)
 
     def status(self, stream=None) -> int:
-        return self.engine.status(stream)
+        with self._on_device():
+            return self.engine.status(stream)

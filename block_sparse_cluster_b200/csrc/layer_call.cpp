@@ -40,7 +40,9 @@ decltype(&da_rope) call_rope = nullptr;
 const Tensor* optional(PyObject* o, const char* what) {
   if (o == Py_None) return nullptr;
   if (!THPVariable_Check(o)) refuse(DA_ERR_INVALID_ARG, std::string(what) + " has to be a tensor");
-  return &THPVariable_Unpack(o);
+  const Tensor& t = THPVariable_Unpack(o);
+  if (t.is_neg()) refuse(DA_ERR_INVALID_ARG, std::string(what) + " is negated lazily (resolve_neg() makes it a plain tensor)");
+  return &t;
 }
 
 const Tensor& tensor(PyObject* o, const char* what) {

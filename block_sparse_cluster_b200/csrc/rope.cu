@@ -10,7 +10,8 @@
 // its sign.  Only the upper 32 bits, as half turns in [-1, 1), are rounded to fp32 for sincospif.
 //
 // A norm whose mean square (with eps) leaves [kLeastMean, fp32's largest number) is taken again of x times a power of two, as
-// the row operators' norms are.
+// the row operators' norms are; behind the loop over the tokens, which only leaves out such heads' stores (a token's sums formed again
+// in the loop cost 40 heads x 75600 tokens 10 us of 265).
 //
 // The kernel is bound by HBM: x is read once and out written once.  A thread's unit of work is two
 // 16-byte vectors of a head, elements [j, j + V) and [j + d/2, j + d/2 + V): whole pairs in either pairing.
@@ -19,8 +20,8 @@
 // of tokens: the block forms the angles of all of them first, and each thread keeps the loads of the next kStages tokens
 // in flight with cp.async, into shared memory that only it reads: loads ahead cost no registers and need no barrier.
 //
-// Measured, bf16, 40 heads of 128 and 75600 tokens (floor 241 us): 240 us without a norm, 246 with the head's, 255 with the
-// norm over all heads, whose barrier a token is what is left; 12 heads, 32760 tokens (floor 31 us): 35, 37 and 42 us, where
+// Measured, bf16, 40 heads of 128 and 75600 tokens (floor 241 us): 240 us without a norm, 246 with the head's, 256 with the
+// norm over all heads, whose barrier a token is what is left; 12 heads, 32880 tokens (floor 31 us): 35, 39 and 44 us, where
 // a token is 96 threads' work of 16 elements and its fixed instructions show.  fp32 runs at the copy's rate.
 #include <math.h>
 
@@ -34,6 +35,7 @@ namespace {
 constexpr int kMaxPairs = 64;   // d <= 128
 constexpr int kMaxRun = 32;     // tokens of a block
 constexpr int kStages = 3;      // tokens a thread holds in flight
+constexpr int kMaxTurns = 16;   // tokens a group takes
 
 enum { kNoNorm = 0, kHeadNorm = 1, kFullNorm = 2 };
 
@@ -159,6 +161,94 @@ __device__ __forceinline__ bool leaves_fp32(float mean) {   // as one comparison
 // than 2^114, and nothing is lost.
 __device__ __forceinline__ float wide_shift(float mean) { return !leaves_fp32(mean) ? 1.f : mean < kLeastMean ? 0x1p100f : 0x1p-72f; }
 
+// The heads or tokens of a run whose squares fp32 loses, which the loop over the tokens has not stored: x still holds them,
+// whether or not out is x.  left: a bit a turn of the thread's group, and for the second of its units (a head's norm) kMaxTurns up.
+// All threads that a sum joins call this together.
+template <typename T, int D, int UPT, bool HALVES>
+__device__ __noinline__ void rope_left(const RopeArgs& a, uint32_t left, int run, const float* s_cos, const int4* s_pos, float* s_wide) {
+  using U = Unit<T, HALVES>;
+  constexpr int V = U::n, kPerHead = D / 2 / V;
+  const int groups = blockDim.x / a.group, g = threadIdx.x / a.group, gt = threadIdx.x - g * a.group;
+  const int h0 = blockIdx.z * a.heads_per_block, units = min(a.heads_per_block, a.H - h0) * kPerHead;
+  const int j = gt % kPerHead * V, head = h0 + gt / kPerHead, joined = a.norm == kHeadNorm ? kPerHead : a.group;
+  const float* const s_sin = s_cos + a.run * (D / 2);
+  auto total = [&](float v) {   // over the threads that a norm joins
+    for (int o = min(joined, 32) / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    if (joined > 32) {
+      if ((threadIdx.x & 31) == 0) s_wide[threadIdx.x >> 5] = v;
+      __syncthreads();
+      v = 0.f;
+      for (int w = 0; w < blockDim.x >> 5; ++w) v += s_wide[w];
+      __syncthreads();
+    }
+    return v;
+  };
+#pragma unroll 1
+  for (int turn = 0; turn * groups < run; ++turn) {
+#pragma unroll 1
+    for (int i0 = 0; i0 < (a.norm == kHeadNorm ? min(UPT, 2) : 1); ++i0) {   // a head's norm: unit by unit; else all of them at once
+      const bool mine = left >> (i0 * kMaxTurns + turn) & 1;
+      if (!__any_sync(0xffffffffu, mine)) continue;
+      const int k = turn * groups + g, n = blockIdx.x * a.run + k, end = a.norm == kHeadNorm ? i0 + 1 : UPT;
+      uint64_t va[V / 2], vb[V / 2];
+      auto load = [&](int i, float shift) {   // of a unit that is there
+        const T* from = static_cast<const T*>(a.x) + blockIdx.y * a.xb + (long long)n * a.xn + (head + i * (a.group / kPerHead)) * a.xh + j;
+        const uint4 raw[2] = {*reinterpret_cast<const uint4*>(from), *reinterpret_cast<const uint4*>(from + D / 2)};
+        U::unpack(raw, va, vb);
+#pragma unroll
+        for (int e = 0; e < V / 2; ++e) {
+          va[e] = f2_mul(va[e], f2_pack(shift, shift));
+          vb[e] = f2_mul(vb[e], f2_pack(shift, shift));
+        }
+      };
+      auto mean_of = [&](float shift) {
+        float ss = 0.f;
+#pragma unroll 1
+        for (int i = i0; i < end; ++i) {
+          if (!mine || gt + i * a.group >= units) continue;
+          load(i, shift);
+          uint64_t s2 = 0;
+#pragma unroll
+          for (int e = 0; e < V / 2; ++e) s2 = f2_fma(va[e], va[e], f2_fma(vb[e], vb[e], s2));
+          float lo, hi;
+          f2_unpack(s2, lo, hi);
+          ss += lo + hi;
+        }
+        return total(ss) * (a.norm == kHeadNorm ? 1.f / D : a.inv_width) + a.eps * shift * shift;
+      };
+      const float shift = wide_shift(mean_of(1.f)), root = rsqrtf(mean_of(shift));
+#pragma unroll 1
+      for (int i = i0; i < end; ++i) {
+        if (!mine || gt + i * a.group >= units) continue;
+        load(i, shift);
+        const T* w = static_cast<const T*>(a.weight) + j + (a.norm == kFullNorm ? (gt + i * a.group) / kPerHead * D : 0);
+        const uint4 wraw[2] = {*reinterpret_cast<const uint4*>(w), *reinterpret_cast<const uint4*>(w + D / 2)};
+        uint64_t wa[V / 2], wb[V / 2], c[V / 2], s[V / 2];
+        U::unpack(wraw, wa, wb);
+#pragma unroll
+        for (int e = 0; e < V / 2; ++e) {
+          va[e] = f2_mul(f2_mul(va[e], f2_pack(root, root)), wa[e]);
+          vb[e] = f2_mul(f2_mul(vb[e], f2_pack(root, root)), wb[e]);
+        }
+        if (s_pos[k].w != 0) {
+#pragma unroll
+          for (int e = 0; e < V / 2; ++e) {
+            const int at = k * (D / 2) + (HALVES ? j + 2 * e : j / 2 + e / (V / 4) * (D / 4) + e % (V / 4) * 2);
+            c[e] = f2_pack(s_cos[at], s_cos[at + 1]);
+            s[e] = f2_pack(s_sin[at], s_sin[at + 1]);
+          }
+          U::rotate(va, vb, c, s);
+        }
+        uint4 o2[2];
+        U::pack(va, vb, o2);
+        T* to = static_cast<T*>(a.out) + blockIdx.y * a.ob + (long long)n * a.on + (head + i * (a.group / kPerHead)) * a.oh + j;
+        *reinterpret_cast<uint4*>(to) = o2[0];
+        *reinterpret_cast<uint4*>(to + D / 2) = o2[1];
+      }
+    }
+  }
+}
+
 // UPT: units a thread holds of a token.
 template <typename T, int D, int UPT, bool HALVES, bool NORMED>
 __global__ void __launch_bounds__(512) rope_kernel(const __grid_constant__ RopeArgs a) {
@@ -245,26 +335,7 @@ __global__ void __launch_bounds__(512) rope_kernel(const __grid_constant__ RopeA
   }
   __syncthreads();
 
-  auto squares = [](const uint4 (&unit)[2]) {
-    uint64_t va[V / 2], vb[V / 2], s2 = 0;
-    U::unpack(unit, va, vb);
-#pragma unroll
-    for (int e = 0; e < V / 2; ++e) s2 = f2_fma(va[e], va[e], f2_fma(vb[e], vb[e], s2));
-    float lo, hi;
-    f2_unpack(s2, lo, hi);
-    return lo + hi;
-  };
-  auto times = [](uint4 (&unit)[2], float shift) {
-    uint64_t va[V / 2], vb[V / 2];
-    U::unpack(unit, va, vb);
-#pragma unroll
-    for (int e = 0; e < V / 2; ++e) {
-      va[e] = f2_mul(va[e], f2_pack(shift, shift));
-      vb[e] = f2_mul(vb[e], f2_pack(shift, shift));
-    }
-    U::pack(va, vb, unit);
-  };
-
+  uint32_t left = 0;   // turns whose units are left to the end (rope_left)
   // every group takes the same number of turns, so that the barriers match
   uint4 raw[UPT][2];
 #pragma unroll
@@ -272,8 +343,9 @@ __global__ void __launch_bounds__(512) rope_kernel(const __grid_constant__ RopeA
   uint4* at = ring;
   T* o = out + (long long)(n0 + g) * a.on;
   const long long out_turn = groups * a.on;
-  for (int k0 = 0, parity = 0; k0 < run; k0 += groups, parity ^= 1, o += out_turn) {
-    const int k = k0 + g;
+  for (int k0 = 0, turn_no = 0; k0 < run; k0 += groups, ++turn_no, o += out_turn) {
+    const int k = k0 + g, parity = turn_no & 1;
+    auto bit = [&](int i) { return 1u << ((i & 1) * kMaxTurns + turn_no); };
     float ss = 0.f, factor[UPT];
     cp_async_wait<kStages - 1>();
 #pragma unroll
@@ -284,7 +356,13 @@ __global__ void __launch_bounds__(512) rope_kernel(const __grid_constant__ RopeA
       }
       factor[i] = 1.f;
       if (NORMED) {
-        factor[i] = squares(raw[i]);
+        uint64_t va[V / 2], vb[V / 2], s2 = 0;
+        U::unpack(raw[i], va, vb);
+#pragma unroll
+        for (int e = 0; e < V / 2; ++e) s2 = f2_fma(va[e], va[e], f2_fma(vb[e], vb[e], s2));
+        float lo, hi;
+        f2_unpack(s2, lo, hi);
+        factor[i] = lo + hi;
         ss += factor[i];
       }
     }
@@ -293,16 +371,9 @@ __global__ void __launch_bounds__(512) rope_kernel(const __grid_constant__ RopeA
       for (int i = 0; i < UPT; ++i) {
 #pragma unroll
         for (int o = kPerHead / 2; o > 0; o >>= 1) factor[i] += __shfl_xor_sync(0xffffffffu, factor[i], o);
-        float mean = factor[i] * (1.f / D) + a.eps;
-        if (__any_sync(0xffffffffu, has(i) && leaves_fp32(mean))) {
-          const float shift = wide_shift(mean);
-          times(raw[i], shift);
-          float s2 = squares(raw[i]);
-#pragma unroll
-          for (int o = kPerHead / 2; o > 0; o >>= 1) s2 += __shfl_xor_sync(0xffffffffu, s2, o);
-          mean = s2 * (1.f / D) + a.eps * shift * shift;
-        }
+        const float mean = factor[i] * (1.f / D) + a.eps;
         factor[i] = rsqrtf(mean);
+        if (k < run && has(i) && leaves_fp32(mean)) left |= bit(i);
       }
     } else if (NORMED) {
       for (int o = min(a.group, 32) / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
@@ -315,25 +386,8 @@ __global__ void __launch_bounds__(512) rope_kernel(const __grid_constant__ RopeA
           ss += (p.x + p.y) + (p.z + p.w);
         }
       }
-      float mean = ss * a.inv_width + a.eps;
-      if (__any_sync(0xffffffffu, leaves_fp32(mean))) {   // in all warps of a block that is the group
-        const float shift = wide_shift(mean);
-        ss = 0.f;
-#pragma unroll
-        for (int i = 0; i < UPT; ++i) {
-          times(raw[i], shift);
-          ss += squares(raw[i]);
-        }
-        for (int o = min(a.group, 32) / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-        if (a.group > 32) {   // the next sum comes here only behind the next token's barrier
-          if ((threadIdx.x & 31) == 0) s_wide[threadIdx.x >> 5] = ss;
-          __syncthreads();
-          ss = 0.f;
-          for (int w = 0; w < blockDim.x >> 5; ++w) ss += s_wide[w];
-        }
-        mean = ss * a.inv_width + a.eps * shift * shift;
-      }
-      const float f = rsqrtf(mean);
+      const float mean = ss * a.inv_width + a.eps, f = rsqrtf(mean);
+      if (k < run && leaves_fp32(mean)) left |= bit(0) | bit(1);
 #pragma unroll
       for (int i = 0; i < UPT; ++i) factor[i] = f;
     }
@@ -355,7 +409,7 @@ __global__ void __launch_bounds__(512) rope_kernel(const __grid_constant__ RopeA
       }
 #pragma unroll
       for (int i = 0; i < UPT; ++i) {
-        if (!has(i)) continue;
+        if (!has(i) || (NORMED && left & bit(i))) continue;
         uint64_t va[V / 2], vb[V / 2];
         U::unpack(raw[i], va, vb);
         if (NORMED) {
@@ -379,6 +433,7 @@ __global__ void __launch_bounds__(512) rope_kernel(const __grid_constant__ RopeA
     fetch(k + kStages * groups, at);   // into the stage that this turn has read
     at = at == ring + (kStages - 1) * stage ? ring : at + stage;
   }
+  if (NORMED && __any_sync(0xffffffffu, left != 0)) rope_left<T, D, UPT, HALVES>(a, left, run, s_cos, s_pos, s_wide);
 }
 
 template <typename T, int D, int UPT>
@@ -420,7 +475,7 @@ cudaError_t launch_typed(RopeArgs& a, int B, cudaStream_t s) {
   // their warps longer runs pay (40 heads: 255 us with 16 tokens, 267 with 8, 268 with 32; without the norm 239 with 8, 242
   // with 16).
   const long long tokens = (long long)B * a.N, blocks = 148 * (upt >= 2 && threads > 128 ? 8 : 16);
-  const int most = upt >= 2 && a.norm == kFullNorm ? 16 : 8;
+  const int most = upt >= 2 && a.norm == kFullNorm ? kMaxTurns : 8;
   int per_group = 1;
   while (per_group < most && groups * per_group * 2 <= kMaxRun && tokens / (groups * per_group * 2) >= blocks) per_group *= 2;
   a.run = groups * per_group;

@@ -328,7 +328,8 @@ def da_noalloc_device_status(stream=None) -> int:
 
 # Operators of the layer around the attention.  They take strided tensors, so their marshalling also reads
 # shapes, strides and devices, in a compiled module (csrc/layer_call.cpp), since the smallest of these calls are bound by
-# the host.  They run on the tensors' device, on its current stream by default.
+# the host.  They run on the tensors' device, on its current stream by default.  They have no backward pass: outputs carry
+# no gradient.
 
 class _Unloaded:
     """In the module's place when it does not load (built for another torch, say): the attention needs none of it."""

@@ -7,8 +7,8 @@
 // together and writes them where the 128-byte swizzle puts them.  A CTA forms 128 x n outputs (n = 128, or 64 or 32 where that
 // fills the GPU) from slices of 128 deep in two buffers: a slice's words are loaded into registers while the one before is
 // multiplied.  Two CTAs an SM.  The loads bound it, by their latency where there are few tiles and by their number where there
-// are many.  Measured, bf16 out: 777 x 1537 x 1001 18 us, 2048 x 5120 x 5121 173 us, 8192 x 5120 x 5121 607 us (7.1e14 op/s, a
-// quarter of the rate of rows on 16 bytes; four products an instruction on the CUDA cores reached 8e13).  Taking a thread's second
+// are many.  Measured, bf16 out: 777 x 1537 x 1001 18 us, 2048 x 5120 x 5121 173-183 us, 8192 x 5120 x 5121 607-620 us (7e14 op/s, a
+// quarter of the rate of rows on 16 bytes; one row of x, 1 x 5120 x 5121, still takes 46 us; four products an instruction on the CUDA cores reached 8e13).  Taking a thread's second
 // word from its neighbour by shuffles halves the loads and was slower (950 us against 840 then); full
 // tiles without a test a chunk are faster (722 -> 607).  The quantisers write rows that need none of it.
 #include "da_common.cuh"

@@ -27,7 +27,7 @@
 //
 // Measured, bf16 out: 75600 x 5120 x 5120 1.22 ms cold and 1.31-1.39 ms in a long run under the power cap (3.24e15 and
 // 2.85-3.0e15 op/s; twice the bf16 library rate is 3.38e15 and 2.87e15), the tensor pipe 94 % busy; 2048 x 5120 x 5120
-// 36 us, 512: 15 us, 128: 10 us.  32760 x 1536 x 1536 59-61 us (2.6e15): at shallow depths the epilogue is what bounds.
+// 37 us, 512: 14 us, 128: 11 us.  32760 x 1536 x 1536 59-61 us (2.6e15): at shallow depths the epilogue is what bounds.
 #include "da_common.cuh"
 #include "da_internal.h"
 #include "linear_i8.cuh"

@@ -1,9 +1,10 @@
 """A transformer layer's attention around the decoupled sparse attention step, in 8-bit weights.
 
 ``DecoupledLayer`` takes hidden states instead of Q, K and V: it adds them to the residual stream,
-norms them, projects them with 8-bit integer products, turns queries and keys by their rotary
-positions, runs Reassign Cache and the decoupled attention, and projects the output back.  Every
-step is one call of the library's operators; this module owns the buffers between them.
+norms them (a root-mean-square norm of fixed weight: no shift, no scale per sample, no gate),
+projects them with 8-bit integer products, turns queries and keys by their rotary positions, runs
+Reassign Cache and the decoupled attention, and projects the output back.  Every step is one call
+of the library's operators; this module owns the buffers between them.
 """
 from __future__ import annotations
 

@@ -117,3 +117,52 @@ def test_rope_after_a_norm_of_any_size(B, H, N, d, axes, norm, dtype, eps):
             out[zero] = 0
         with np.errstate(divide="ignore", invalid="ignore"):
             _rope_check(x, out, rope, None, weight, max(eps, 1e-300), dtype)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("width", [64, 77, 1002, 1536, 4100, 9002, 16384])
+def test_wide_rows_in_place(width, dtype):
+    """The norm's output and its sum in the inputs' buffers, either way round, and the codes' sum in x: the bits of separate buffers."""
+    x, r, w = (t.cuda() for t in _rows(width, dtype, width + 1))
+    out, total = torch.empty_like(x), torch.empty_like(x)
+    da.da_rms_norm(x, w, out, residual=r, sum_out=total, eps=0.0)
+    for out_is_x in (True, False):
+        xc, rc = x.clone(), r.clone()
+        da.da_rms_norm(xc, w, xc if out_is_x else rc, residual=rc, sum_out=rc if out_is_x else xc, eps=0.0)
+        got_out, got_sum = (xc, rc) if out_is_x else (rc, xc)
+        assert torch.equal(got_out.nan_to_num(7.0), out.nan_to_num(7.0)) and torch.equal(got_sum, total)
+    q, scale = torch.empty(x.shape, dtype=torch.int8, device="cuda"), torch.empty(x.shape[0], device="cuda")
+    q2, scale2 = torch.empty_like(q), torch.empty_like(scale)
+    da.da_rms_norm_i8(x, w, q, scale, residual=r, sum_out=total, eps=0.0)
+    xc = x.clone()
+    da.da_rms_norm_i8(xc, w, q2, scale2, residual=r, sum_out=xc, eps=0.0)
+    assert torch.equal(q, q2) and torch.equal(scale, scale2) and torch.equal(xc, total)
+
+
+@pytest.mark.parametrize("B,H,N,d,norm,dtype", [
+    (1, 12, 19003, 128, "full", BF16), (1, 40, 19003, 128, "full", BF16), (2, 12, 9507, 128, "head", BF16), (1, 8, 76001, 128, "head", BF16),
+    (1, 4, 76003, 128, "full", BF16), (1, 12, 19001, 128, "full", F32), (1, 3, 38001, 64, "head", F32), (1, 70, 9601, 128, "full", F32),
+])
+def test_rope_of_long_runs_with_values_of_any_size(B, H, N, d, norm, dtype):
+    """A third of the heads or tokens outside fp32's squares, anywhere in a run: short calls' bits, the oracle's values, and in place."""
+    g = _gen(N)
+    rope = da.Rope(axes=(44, 42, 42) if d == 128 else (20, 22, 22), pairing="halves" if H == 12 else "adjacent")
+    power = torch.tensor([1.0, 2.0 ** 80, 2.0, 2.0 ** -90, 0.5, 3.0])
+    which = torch.randint(0, 6, (B, 1 if norm == "full" else H, N, 1), generator=g)
+    buf = torch.randn(B, N, 2, H, d, generator=g).to(dtype).cuda()
+    x = buf[:, :, 0].permute(0, 2, 1, 3)
+    x.mul_(power.cuda()[which.cuda()].to(dtype))
+    weight = (1 + 0.2 * torch.randn(d if norm == "head" else H * d, generator=g)).to(dtype).cuda()
+    pos = torch.randint(-5000, 1 << 20, (N, 3), generator=g, dtype=torch.int32).cuda()
+    out = torch.empty(B, H, N, d, dtype=dtype, device="cuda")
+    da.da_rope(x, out, rope, positions=pos, weight=weight, eps=0.0)
+    some = torch.cat([torch.arange(40), torch.randint(0, N, (40,), generator=g), N - 1 - torch.arange(40)]).unique().cuda()
+    _rope_check(x[:, :, some], out[:, :, some], rope, pos[some].contiguous(), weight, 0.0, dtype)
+    for lo in range(0, N, 1000):
+        hi = min(lo + 1000, N)
+        part = torch.empty(B, H, hi - lo, d, dtype=dtype, device="cuda")
+        da.da_rope(x[:, :, lo:hi], part, rope, positions=pos[lo:hi].contiguous(), weight=weight, eps=0.0)
+        assert torch.equal(part, out[:, :, lo:hi]), lo
+    other = buf[:, :, 1].clone()
+    da.da_rope(x, x, rope, positions=pos, weight=weight, eps=0.0)
+    assert torch.equal(x, out) and torch.equal(buf[:, :, 1], other)
